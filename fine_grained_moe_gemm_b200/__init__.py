@@ -26,7 +26,7 @@ _DEFAULT_LIB_PATH = LIB_PATH
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE, MOE_ERR_CUDA = range(6)
-MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_F16 = 0, 1, 2, 3
 MOE_DEVERR_BAD_EXPERT, MOE_DEVERR_TIMEOUT, MOE_DEVERR_BAD_ROWS, MOE_DEVERR_NONFINITE, MOE_DEVERR_BOUNDS = 1, 2, 4, 8, 16
 MOE_DEBUG_TABLE_ROW_TOK, MOE_DEBUG_TABLE_ROW_OFF = 0, 1
 
@@ -127,6 +127,19 @@ def _configure(L):
     L.moe_ep_combine_peer.argtypes = [I, I, I, I, I, P, P, P, P, P, P]
     L.moe_forward_noalloc.restype = I
     L.moe_forward_noalloc.argtypes = [ctypes.POINTER(MoeConfig), ctypes.POINTER(MoeWeights), P, P, I, P, I, I, P]
+    LL = ctypes.c_int64
+    L.moe_grouped_mm.restype = I
+    L.moe_grouped_mm.argtypes = [I, I, I, I, I, P, LL, P, I, P, P, LL, I, I, P]
+    L.moe_grouped_wgrad.restype = I
+    L.moe_grouped_wgrad.argtypes = [I, I, I, I, I, P, LL, P, LL, P, P, I, I, P]
+    L.moe_swiglu.restype = I
+    L.moe_swiglu.argtypes = [I, I, I, P, LL, P, LL, P, P, P, LL, P]
+    L.moe_swiglu_backward.restype = I
+    L.moe_swiglu_backward.argtypes = [I, I, I, P, LL, P, LL, P, LL, P, P, P, LL, P, LL, P, P]
+    L.moe_quantize_int8.restype = I
+    L.moe_quantize_int8.argtypes = [P, I, LL, I, I, P, P, P, P]
+    L.moe_grouped_mm_int8.restype = I
+    L.moe_grouped_mm_int8.argtypes = [I, I, I, I, P, P, P, P, P, P, LL, I, I, P]
     L.moe_debug_build.restype = I
     L.moe_debug_build.argtypes = []
     L.moe_debug_corrupt_next.restype = I
@@ -636,6 +649,141 @@ def moe_quantize_act(x, q, sx, stream=None):
         _dev(t, n)
     T, d = x.shape
     _check(lib().moe_quantize_act(_p(x), T, d, _p(q), _p(sx), _stream(stream)), "moe_quantize_act")
+
+
+# ---------------------------------------------------------------- products by group
+_FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _rows(t, name: str, shape, dtypes) -> int:
+    """Checks a 2-D CUDA tensor whose rows may lie apart (a slice of a wider buffer); returns their distance."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    _shape(t, name, shape, dtypes)
+    if t.shape[0] <= 1:  # one row or none: torch leaves the stride open
+        step = 16 // t.element_size()
+        return (t.shape[1] + step - 1) // step * step
+    return t.stride(0)
+
+
+def _offsets(offsets, groups: int):
+    if offsets is None:
+        if groups != 1:
+            raise ValueError("offsets: only one group can go without")
+        return
+    _dev(offsets, "offsets")
+    _shape(offsets, "offsets", (groups + 1,), (torch.int32,))
+
+
+def _count(n_rows):
+    if n_rows is not None:
+        _dev(n_rows, "n_rows")
+        if n_rows.dtype != torch.int32 or n_rows.numel() != 1:
+            raise ValueError("n_rows: one int32 on the device")
+
+
+def moe_grouped_mm(x, w, offsets, y, transpose_w: bool = False, accumulate: bool = False, stream=None):
+    """y[r] (+)= x[r] . w[g]^T for the rows r of each group g (``offsets`` [G+1] int32; None: one group of all rows).
+    x [R, k], w [G, n, k] (``transpose_w``: [G, k, n], the product with w itself, which is the input gradient of the
+    other form), bf16 or f16; y [R, n] of that type or fp32.  Rows of x and y may be slices of wider buffers; rows
+    outside the groups are left as they were."""
+    _dev(w, "w")
+    if w.dim() != 3 or w.dtype not in _HALVES:
+        raise ValueError(f"w: {tuple(w.shape)} {w.dtype}, expected three dimensions, bf16 or f16")
+    G, n, k = w.shape
+    if transpose_w:
+        n, k = k, n
+    R = x.shape[0]
+    ldx = _rows(x, "x", (R, k), (w.dtype,))
+    ldy = _rows(y, "y", (R, n), (w.dtype, torch.float32))
+    _offsets(offsets, G)
+    _check(lib().moe_grouped_mm(G, R, n, k, _FLOATS[w.dtype], _p(x), ldx, _p(w), 1 if transpose_w else 0, _p(offsets),
+                                _p(y), ldy, _FLOATS[y.dtype], 1 if accumulate else 0, _stream(stream)),
+           "moe_grouped_mm")
+
+
+def moe_grouped_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=None):
+    """dw[g] (+)= dy[rows of g]^T . x[rows of g]: the weight gradient of ``moe_grouped_mm``.  dy [R, n] and x [R, k]
+    bf16 or f16; dw [G, n, k] of that type or fp32; an empty group's gradient is zero."""
+    _dev(dw, "dw")
+    if dw.dim() != 3:
+        raise ValueError(f"dw: {tuple(dw.shape)}, expected three dimensions")
+    G, n, k = dw.shape
+    R = x.shape[0]
+    ldx = _rows(x, "x", (R, k), _HALVES)
+    lddy = _rows(dy, "dy", (R, n), (x.dtype,))
+    _shape(dw, "dw", (G, n, k), (x.dtype, torch.float32))
+    _offsets(offsets, G)
+    _check(lib().moe_grouped_wgrad(G, R, n, k, _FLOATS[x.dtype], _p(dy), lddy, _p(x), ldx, _p(offsets), _p(dw),
+                                   _FLOATS[dw.dtype], 1 if accumulate else 0, _stream(stream)), "moe_grouped_wgrad")
+
+
+def _coef(t, name: str, R: int):
+    if t is not None:
+        _dev(t, name)
+        _shape(t, name, (R,), (torch.float32,))
+
+
+def moe_swiglu(gate, up, h, coef=None, n_rows=None, stream=None):
+    """h = coef * SiLU(gate) * up per row ([R, width], fp32, bf16 or f16; coef fp32 [R] or None).  ``n_rows``: one
+    int32 on the device, the rows to compute (e.g. ``offsets[-1:]``); the rows behind are left as they were.  h may
+    be gate or up."""
+    shape, t = tuple(gate.shape), (gate.dtype,)
+    ldg = _rows(gate, "gate", shape, tuple(_FLOATS))
+    ldu, ldh = _rows(up, "up", shape, t), _rows(h, "h", shape, t)
+    _coef(coef, "coef", shape[0])
+    _count(n_rows)
+    _check(lib().moe_swiglu(shape[0], shape[1], _FLOATS[gate.dtype], _p(gate), ldg, _p(up), ldu, _p(coef), _p(n_rows),
+                            _p(h), ldh, _stream(stream)), "moe_swiglu")
+
+
+def moe_swiglu_backward(dh, gate, up, dgate, dup, coef=None, dcoef=None, n_rows=None, stream=None):
+    """The gradients of ``moe_swiglu``: dgate, dup (like gate), and dcoef fp32 [R] when given.  dgate may be gate,
+    dup may be up or dh."""
+    shape, t = tuple(gate.shape), (gate.dtype,)
+    ldg = _rows(gate, "gate", shape, tuple(_FLOATS))
+    lds = [_rows(v, name, shape, t) for name, v in (("dh", dh), ("up", up), ("dgate", dgate), ("dup", dup))]
+    _coef(coef, "coef", shape[0])
+    _coef(dcoef, "dcoef", shape[0])
+    _count(n_rows)
+    _check(lib().moe_swiglu_backward(shape[0], shape[1], _FLOATS[gate.dtype], _p(dh), lds[0], _p(gate), ldg, _p(up),
+                                     lds[1], _p(coef), _p(n_rows), _p(dgate), lds[2], _p(dup), lds[3], _p(dcoef),
+                                     _stream(stream)), "moe_swiglu_backward")
+
+
+def moe_quantize_int8(x, q, sx, n_rows=None, stream=None):
+    """int8 codes q [R, k] and fp32 scales sx [R] of the rows of x [R, k] (fp32, bf16 or f16): sx = max|x| / 127, q the
+    nearest integer of x / sx, ties to even.  Weights [.., n, k] quantise per output channel through a view of
+    their rows."""
+    R, k = x.shape
+    ldx = _rows(x, "x", (R, k), tuple(_FLOATS))
+    for name, t, shape, dt in (("q", q, (R, k), torch.int8), ("sx", sx, (R,), torch.float32)):
+        _dev(t, name)
+        _shape(t, name, shape, (dt,))
+    _count(n_rows)
+    _check(lib().moe_quantize_int8(_p(x), _FLOATS[x.dtype], ldx, R, k, _p(n_rows), _p(q), _p(sx), _stream(stream)),
+           "moe_quantize_int8")
+
+
+def moe_grouped_mm_int8(q, sx, w, sw, offsets, y, accumulate: bool = False, stream=None):
+    """y[r] (+)= sx[r] sw[g] (q[r] . w[g]^T) with exact integer sums: q [R, k], w [G, n, k] int8, sx [R], sw [G, n]
+    fp32, y [R, n] fp32, bf16 or f16; offsets as in ``moe_grouped_mm``."""
+    for name, t in (("q", q), ("sx", sx), ("w", w), ("sw", sw)):
+        _dev(t, name)
+    if w.dim() != 3:
+        raise ValueError(f"w: {tuple(w.shape)}, expected three dimensions")
+    G, n, k = w.shape
+    R = q.shape[0]
+    for name, t, shape, dt in (("q", q, (R, k), torch.int8), ("sx", sx, (R,), torch.float32), ("w", w, (G, n, k), torch.int8),
+                               ("sw", sw, (G, n), torch.float32)):
+        _shape(t, name, shape, (dt,))
+    ldy = _rows(y, "y", (R, n), tuple(_FLOATS))
+    _offsets(offsets, G)
+    _check(lib().moe_grouped_mm_int8(G, R, n, k, _p(q), _p(sx), _p(w), _p(sw), _p(offsets), _p(y), ldy,
+                                     _FLOATS[y.dtype], 1 if accumulate else 0, _stream(stream)), "moe_grouped_mm_int8")
 
 
 def device_error(stream=None) -> int:

@@ -12,8 +12,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
-SOURCES = ["moe_kernels.cu", "moe_api.cu", "moe_noalloc.cu"]
-HEADERS = ["moe_device.cuh", "moe_gemm.cuh", "moe_gemm_fp8.cuh", "moe_gemm2.cuh", "moe_gemm2_fp8.cuh", "moe_launch.h", os.path.join("..", "..", "include", "moe.h")]
+SOURCES = ["moe_kernels.cu", "moe_api.cu", "moe_products.cu", "moe_noalloc.cu"]
+HEADERS = ["moe_device.cuh", "moe_gemm.cuh", "moe_gemm_fp8.cuh", "moe_gemm2.cuh", "moe_gemm2_fp8.cuh", "moe_ragged.cuh",
+           "moe_rows.cuh", "moe_host.h", "moe_launch.h", os.path.join("..", "..", "include", "moe.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

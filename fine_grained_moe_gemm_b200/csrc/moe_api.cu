@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "moe_host.h"
 #include "moe_launch.h"
 
 #ifdef MOE_DEBUG
@@ -31,8 +32,6 @@ using namespace moe;
 namespace {
 
 // ------------------------------------------------------------------ checks
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 moe_status check_config(const moe_config* c) {
     if (!c) return MOE_ERR_INVALID_ARG;
     if (c->d <= 0 || c->d % 128 != 0) return MOE_ERR_INVALID_ARG;
@@ -50,54 +49,7 @@ moe_status check_config(const moe_config* c) {
     return MOE_OK;
 }
 
-struct DevInfo {
-    int sm_count = 0;
-    int major = 0;
-};
-
-DevInfo dev_info() {
-    static std::mutex mu;
-    static DevInfo cache[64];
-    static bool have[64] = {};
-    int dev = 0;
-    DevInfo info;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return info;
-    std::lock_guard<std::mutex> g(mu);
-    if (dev < 64 && have[dev]) return cache[dev];
-    cudaDeviceGetAttribute(&info.sm_count, cudaDevAttrMultiProcessorCount, dev);
-    cudaDeviceGetAttribute(&info.major, cudaDevAttrComputeCapabilityMajor, dev);
-    if (dev < 64) {
-        cache[dev] = info;
-        have[dev] = true;
-    }
-    return info;
-}
-
-moe_status check_device(DevInfo* out) {
-    DevInfo i = dev_info();
-    if (i.major != 10 || i.sm_count <= 0) return MOE_ERR_UNSUPPORTED;
-    *out = i;
-    return MOE_OK;
-}
-
 // ------------------------------------------------------------------ TMA maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // 2-D row-major [rows, cols] map, box [box_rows, box_cols], 128-byte swizzle,
 // out-of-bounds elements read as zero.
 bool map_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, const void* ptr, uint64_t rows, uint64_t cols,
@@ -231,19 +183,6 @@ Workspace layout(const moe_config* c, int T, void* base) {
     w.bytes = off;
     return w;
 }
-
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-// NVTX ranges around the host-side enqueue of each stage (names "moe.<stage>"),
-// nested in one range per entry point: a profiler's timeline groups the kernels
-// by stage, and ncu can select them with --nvtx-include.  Header-only NVTX: with
-// no tool attached each push/pop is a call through a null stub.
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange&) = delete;
-    NvtxRange& operator=(const NvtxRange&) = delete;
-};
 
 // Consecutive stages of one call: next() closes the open stage range, if any,
 // and opens the named one; the destructor closes the last.

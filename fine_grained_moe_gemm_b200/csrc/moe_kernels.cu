@@ -17,6 +17,9 @@
 //   rmsnorm_kernel        pre-norm of the sublayer (+ the 1x128 e4m3 quantisation)
 //   dense_schedule_kernel the one-group tables of the dense FFN
 //   finalize_kernel       fp32 combine buffer -> bf16 output (+ residual)
+//   moe_ragged_kernel     products grouped by expert: projections, input and weight
+//                         gradients, 8-bit integers (moe_ragged.cuh)
+//   swiglu_kernel, swiglu_backward_kernel, quantize_int8_kernel  row operators (moe_rows.cuh)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,6 +34,8 @@
 #include "moe_gemm2.cuh"
 #include "moe_gemm2_fp8.cuh"
 #include "moe_launch.h"
+#include "moe_ragged.cuh"
+#include "moe_rows.cuh"
 
 namespace moe {
 
@@ -1369,6 +1374,77 @@ cudaError_t launch_ep_combine(const float* back, const int32_t* send_tok, int n_
     if (grid > (size_t)n_sm * 16) grid = (size_t)n_sm * 16;
     note_launch();
     ep_combine_kernel<<<(unsigned)grid, 256, 0, s>>>(back, send_tok, n_rows, T, d, acc, src_rank, capacity, src_row0);
+    return cudaGetLastError();
+}
+
+template <int DIR, bool I8>
+static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_t s) {
+    constexpr int smem = RagCfg<DIR>::SMEM_BYTES;
+    static std::atomic<bool> attr_set[64];  // once per device (a repeated set is harmless)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
+        cudaError_t e = cudaFuncSetAttribute(moe_ragged_kernel<DIR, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
+    }
+    note_launch();
+    moe_ragged_kernel<DIR, I8><<<grid, RAG_THREADS, smem, s>>>(*args);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s) {
+    grid &= ~1;
+    if (grid < 2) return cudaErrorInvalidValue;
+    if (i8) return dir == RAG_NT ? launch_ragged_t<RAG_NT, true>(args, grid, s) : cudaErrorInvalidValue;
+    if (dir == RAG_NT) return launch_ragged_t<RAG_NT, false>(args, grid, s);
+    if (dir == RAG_NN) return launch_ragged_t<RAG_NN, false>(args, grid, s);
+    return dir == RAG_TN ? launch_ragged_t<RAG_TN, false>(args, grid, s) : cudaErrorInvalidValue;
+}
+
+template <typename T>
+static void launch_swiglu_t(bool backward, const SwigluArgs& a, int n_sm, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const int vecs = a.width / V;
+    int tx = 8;
+    while (tx < vecs && tx < ROWS_THREADS) tx *= 2;
+    const int rows_per_cta = ROWS_THREADS / tx;
+    const int want = (a.rows + rows_per_cta - 1) / rows_per_cta;
+    const int grid = want < n_sm * 8 ? want : n_sm * 8;
+    note_launch();
+    if (backward) swiglu_backward_kernel<T><<<grid, ROWS_THREADS, 0, s>>>(a, tx);
+    else swiglu_kernel<T><<<grid, ROWS_THREADS, 0, s>>>(a, tx);
+}
+
+cudaError_t launch_swiglu(bool backward, moe_dtype t, const SwigluArgs& a, int n_sm, cudaStream_t s) {
+    if (t == MOE_BF16) launch_swiglu_t<__nv_bfloat16>(backward, a, n_sm, s);
+    else if (t == MOE_F16) launch_swiglu_t<__half>(backward, a, n_sm, s);
+    else launch_swiglu_t<float>(backward, a, n_sm, s);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static void launch_quantize_t(const void* x, long long ldx, int rows, int k, const int* n_rows, int8_t* q, float* sx,
+                              int n_sm, cudaStream_t s) {
+    const int vecs = k / 16;
+    int tx = 32;
+    while (tx * 4 < vecs) tx *= 2;  // at most 512: k <= 32768
+    const int ty = tx < 128 ? 128 / tx : 1;
+    const int want = (rows + ty - 1) / ty;
+    const int grid = want < n_sm * 16 ? want : n_sm * 16;
+    const int nv = (vecs + tx - 1) / tx;
+    note_launch();
+    if (nv <= 1) quantize_int8_kernel<T, 1><<<grid, tx * ty, 0, s>>>(static_cast<const T*>(x), ldx, rows, k, n_rows, q, sx, tx);
+    else if (nv <= 2) quantize_int8_kernel<T, 2><<<grid, tx * ty, 0, s>>>(static_cast<const T*>(x), ldx, rows, k, n_rows, q, sx, tx);
+    else quantize_int8_kernel<T, 4><<<grid, tx * ty, 0, s>>>(static_cast<const T*>(x), ldx, rows, k, n_rows, q, sx, tx);
+}
+
+cudaError_t launch_quantize_int8(const void* x, moe_dtype t, long long ldx, int rows, int k, const int* n_rows,
+                                 int8_t* q, float* sx, int n_sm, cudaStream_t s) {
+    if (t == MOE_BF16) launch_quantize_t<__nv_bfloat16>(x, ldx, rows, k, n_rows, q, sx, n_sm, s);
+    else if (t == MOE_F16) launch_quantize_t<__half>(x, ldx, rows, k, n_rows, q, sx, n_sm, s);
+    else launch_quantize_t<float>(x, ldx, rows, k, n_rows, q, sx, n_sm, s);
     return cudaGetLastError();
 }
 

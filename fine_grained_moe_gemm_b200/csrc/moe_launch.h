@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moe.h"
+
 namespace moe {
 
 // Arguments of the grouped GEMM kernel (moe_gemm.cuh), passed by value.
@@ -157,5 +159,45 @@ constexpr int NORM_MAX_VEC = 8;  // 8-feature vectors per thread: d <= 8 * 8 * 1
 cudaError_t launch_rmsnorm(const __nv_bfloat16* h, const __nv_bfloat16* g, int T, int d, float eps,
                            __nv_bfloat16* out, uint8_t* q, float* sx, cudaStream_t s);
 cudaError_t read_clear_dev_error(unsigned int* flags, cudaStream_t s);
+
+
+// ---------------------------------------------------------------- products by group (moe_ragged.cuh)
+enum { RAG_NT = 0, RAG_NN = 1, RAG_TN = 2 };
+constexpr int RAG_MAX_GROUPS = 1024;
+
+struct RaggedArgs {
+    CUtensorMap a;     // NT: w [groups][n][k] (box 128 rows), NN: w [groups][k][n] (64 x 64), TN: dy [rows, n] (64 x 64)
+    CUtensorMap b128;  // NT, NN: x [rows, k] in boxes of 128 / 64 / 16 rows; TN: b64 = x [rows, k] (64 x 64)
+    CUtensorMap b64;
+    CUtensorMap b16;
+    const int* offsets;    // [groups + 1]; NULL: one group of all rows
+    int groups, rows, n, k;
+    int bf16;              // 16-bit operands: 1 bf16, 0 f16
+    void* y;               // NT, NN: [rows, n] with rows ldy apart; TN: dw [groups][n][k]
+    long long ldy;
+    int out;               // MOE_F32, MOE_BF16 or MOE_F16
+    int accumulate;
+    const float* sx;       // 8-bit operands: scale of each row, and of each [group][n]
+    const float* sw;
+};
+
+cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s);
+
+// ---------------------------------------------------------------- rows (moe_rows.cuh)
+struct SwigluArgs {
+    const void* gate;
+    const void* up;
+    const void* dh;     // backward
+    void* out0;         // forward: h; backward: dgate
+    void* out1;         // backward: dup
+    const float* coef;  // [rows] or NULL (1)
+    float* dcoef;       // backward: [rows] or NULL
+    const int* n_rows;  // device: rows to compute, or NULL (all)
+    long long ld_gate, ld_up, ld_dh, ld_out0, ld_out1;
+    int rows, width;
+};
+cudaError_t launch_swiglu(bool backward, moe_dtype t, const SwigluArgs& a, int n_sm, cudaStream_t s);
+cudaError_t launch_quantize_int8(const void* x, moe_dtype t, long long ldx, int rows, int k, const int* n_rows,
+                                 int8_t* q, float* sx, int n_sm, cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,247 @@
+// C ABI of the products grouped by expert and the row operators around them
+// (include/moe.h): argument checks, tensor maps, launches.  Host code only.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "../../include/moe.h"
+#include "moe_host.h"
+#include "moe_launch.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kMaxWidth = 65536;     // n, k: 128 * 128 * 65536 = 2^30, so 8-bit sums stay inside 32 bits
+constexpr int kMaxRows = 1 << 24;    // items of all groups stay inside 32 bits
+constexpr int kMaxQuantWidth = 32768;  // a row in registers: 512 threads of four 16-value pieces
+constexpr int64_t kMaxLd = 1ll << 36;
+
+int size_of(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
+bool is_float(moe_dtype t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
+moe_status refused(moe_dtype t) { return is_float(t) || t == MOE_E4M3 ? MOE_ERR_UNSUPPORTED : MOE_ERR_INVALID_ARG; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// distance of rows: holds a row and keeps every row on a 16-byte boundary
+bool good_ld(int64_t ld, int width, int elem) { return ld >= width && ld <= kMaxLd && (ld * elem) % 16 == 0; }
+
+// Shapes and flags that every product checks; k_step: elements of 16 bytes of the operands.
+moe_status check_product(int groups, int rows, int n, int k, int k_step, const int32_t* offsets, moe_dtype out,
+                         moe_dtype operands, int accumulate) {
+    if (groups < 1 || groups > RAG_MAX_GROUPS || rows < 0 || rows > kMaxRows) return MOE_ERR_INVALID_ARG;
+    if (n < 8 || n > kMaxWidth || n % 8 != 0 || k < k_step || k > kMaxWidth || k % k_step != 0)
+        return MOE_ERR_INVALID_ARG;
+    if ((!offsets && groups != 1) || !aligned4(offsets) || (accumulate != 0 && accumulate != 1))
+        return MOE_ERR_INVALID_ARG;
+    if (!is_float(out)) return MOE_ERR_INVALID_ARG;
+    if (out != MOE_F32 && out != operands) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// Tiled map of 128-byte-swizzled boxes over [depth][rows][cols] (depth 0: two
+// dimensions), rows ld elements apart; elements outside read as zero.
+bool map_box(CUtensorMap* m, CUtensorMapDataType dt, int elem, const void* p, uint64_t depth, uint64_t rows,
+             uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {cols, rows, depth};
+    const cuuint64_t strides[2] = {ld * elem, ld * elem * rows};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / elem), box_rows, 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return enc(m, dt, depth ? 3 : 2, const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+CUtensorMapDataType map_type(moe_dtype t) {
+    return t == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// CTAs of a launch: a pair for every SM pair, or fewer when the groups cannot have more items.
+int grid_of(const DevInfo& di, long long most_items) {
+    const long long want = 2 * most_items;
+    return (int)(want < (di.sm_count & ~1) ? want : (di.sm_count & ~1));
+}
+
+moe_status product(bool i8, moe_dtype t, int groups, int rows, int n, int k, const void* x, int64_t ldx, const void* w,
+                   int transpose_w, const float* sx, const float* sw, const int32_t* offsets, void* y, int64_t ldy,
+                   moe_dtype out, int accumulate, moe_stream_t stream) {
+    DevInfo di;
+    const moe_status st = check_device(&di);
+    if (st != MOE_OK) return st;
+    RaggedArgs a;
+    memset(&a, 0, sizeof(a));
+    const int elem = i8 ? 1 : 2;
+    const CUtensorMapDataType dt = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(t);
+    const bool ok = (transpose_w ? map_box(&a.a, dt, elem, w, groups, k, n, n, 64)
+                                 : map_box(&a.a, dt, elem, w, groups, n, k, k, 128)) &&
+                    map_box(&a.b128, dt, elem, x, 0, rows, k, ldx, 128) &&
+                    map_box(&a.b64, dt, elem, x, 0, rows, k, ldx, 64) &&
+                    map_box(&a.b16, dt, elem, x, 0, rows, k, ldx, 16);
+    if (!ok) return MOE_ERR_CUDA;
+    a.offsets = offsets;
+    a.groups = groups;
+    a.rows = rows;
+    a.n = n;
+    a.k = k;
+    a.bf16 = t == MOE_BF16;
+    a.y = y;
+    a.ldy = ldy;
+    a.out = out;
+    a.accumulate = accumulate;
+    a.sx = sx;
+    a.sw = sw;
+    const long long items = (long long)((n + 255) / 256) * (rows / 256 + (groups < rows ? groups : rows));
+    return cuda_status(launch_ragged(transpose_w ? RAG_NN : RAG_NT, i8, &a, grid_of(di, items), (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_mm(int groups, int rows, int n, int k, moe_dtype dtype, const void* x, int64_t ldx,
+                          const void* w, int transpose_w, const int32_t* offsets, void* y, int64_t ldy,
+                          moe_dtype y_dtype, int accumulate, moe_stream_t stream) {
+    NvtxRange nv("moe.grouped_mm");
+    if (dtype != MOE_BF16 && dtype != MOE_F16) return refused(dtype);
+    const moe_status st = check_product(groups, rows, n, k, 8, offsets, y_dtype, dtype, accumulate);
+    if (st != MOE_OK) return st;
+    if (transpose_w != 0 && transpose_w != 1) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    if (!good_ld(ldx, k, 2) || !good_ld(ldy, n, size_of(y_dtype))) return MOE_ERR_INVALID_ARG;
+    return product(false, dtype, groups, rows, n, k, x, ldx, w, transpose_w, nullptr, nullptr, offsets, y, ldy,
+                   y_dtype, accumulate, stream);
+}
+
+moe_status moe_grouped_mm_int8(int groups, int rows, int n, int k, const int8_t* q, const float* sx, const int8_t* w,
+                               const float* sw, const int32_t* offsets, void* y, int64_t ldy, moe_dtype y_dtype,
+                               int accumulate, moe_stream_t stream) {
+    NvtxRange nv("moe.grouped_mm_int8");
+    const moe_status st = check_product(groups, rows, n, k, 16, offsets, y_dtype, y_dtype, accumulate);
+    if (st != MOE_OK) return st;
+    if (rows == 0) return MOE_OK;
+    if (!q || !w || !y || !sx || !sw || !aligned16(q) || !aligned16(w) || !aligned16(y) || !aligned4(sx) ||
+        !aligned4(sw) || !good_ld(ldy, n, size_of(y_dtype)))
+        return MOE_ERR_INVALID_ARG;
+    return product(true, y_dtype, groups, rows, n, k, q, k, w, 0, sx, sw, offsets, y, ldy, y_dtype, accumulate, stream);
+}
+
+moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dtype dtype, const void* dy, int64_t lddy,
+                             const void* x, int64_t ldx, const int32_t* offsets, void* dw, moe_dtype dw_dtype,
+                             int accumulate, moe_stream_t stream) {
+    NvtxRange nv("moe.grouped_wgrad");
+    if (dtype != MOE_BF16 && dtype != MOE_F16) return refused(dtype);
+    moe_status st = check_product(groups, rows, n, k, 8, offsets, dw_dtype, dtype, accumulate);
+    if (st != MOE_OK) return st;
+    if (!dw || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+    if (rows && (!dy || !x || !aligned16(dy) || !aligned16(x) || !good_ld(lddy, n, 2) || !good_ld(ldx, k, 2)))
+        return MOE_ERR_INVALID_ARG;
+    DevInfo di;
+    if ((st = check_device(&di)) != MOE_OK) return st;
+    if (rows == 0) {  // a sum of nothing
+        if (accumulate) return MOE_OK;
+        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)groups * n * k * size_of(dw_dtype), (cudaStream_t)stream));
+    }
+    RaggedArgs a;
+    memset(&a, 0, sizeof(a));
+    if (!map_box(&a.a, map_type(dtype), 2, dy, 0, rows, n, lddy, 64) ||
+        !map_box(&a.b64, map_type(dtype), 2, x, 0, rows, k, ldx, 64))
+        return MOE_ERR_CUDA;
+    a.b128 = a.b16 = a.b64;
+    a.offsets = offsets;
+    a.groups = groups;
+    a.rows = rows;
+    a.n = n;
+    a.k = k;
+    a.bf16 = dtype == MOE_BF16;
+    a.y = dw;
+    a.out = dw_dtype;
+    a.accumulate = accumulate;
+    const long long items = (long long)groups * ((n + 255) / 256) * ((k + 255) / 256);
+    return cuda_status(launch_ragged(RAG_TN, false, &a, grid_of(di, items), (cudaStream_t)stream));
+}
+
+moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* gate, int64_t ld_gate, const void* up,
+                      int64_t ld_up, const float* coef, const int32_t* n_rows, void* h, int64_t ld_h,
+                      moe_stream_t stream) {
+    NvtxRange nv("moe.swiglu");
+    if (!is_float(dtype)) return refused(dtype);
+    if (rows < 0 || rows > kMaxRows || width < 8 || width > kMaxWidth || width % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    const int e = size_of(dtype);
+    if (!gate || !up || !h || !aligned16(gate) || !aligned16(up) || !aligned16(h) || !aligned4(coef) ||
+        !aligned4(n_rows) || !good_ld(ld_gate, width, e) || !good_ld(ld_up, width, e) || !good_ld(ld_h, width, e))
+        return MOE_ERR_INVALID_ARG;
+    DevInfo di;
+    const moe_status st = check_device(&di);
+    if (st != MOE_OK) return st;
+    SwigluArgs a;
+    memset(&a, 0, sizeof(a));
+    a.gate = gate;
+    a.up = up;
+    a.out0 = h;
+    a.coef = coef;
+    a.n_rows = n_rows;
+    a.ld_gate = ld_gate;
+    a.ld_up = ld_up;
+    a.ld_out0 = ld_h;
+    a.rows = rows;
+    a.width = width;
+    return cuda_status(launch_swiglu(false, dtype, a, di.sm_count, (cudaStream_t)stream));
+}
+
+moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, const void* dh, int64_t ld_dh, const void* gate,
+                               int64_t ld_gate, const void* up, int64_t ld_up, const float* coef,
+                               const int32_t* n_rows, void* dgate, int64_t ld_dgate, void* dup, int64_t ld_dup,
+                               float* dcoef, moe_stream_t stream) {
+    NvtxRange nv("moe.swiglu_backward");
+    if (!is_float(dtype)) return refused(dtype);
+    if (rows < 0 || rows > kMaxRows || width < 8 || width > kMaxWidth || width % 8 != 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    const int e = size_of(dtype);
+    if (!dh || !gate || !up || !dgate || !dup || !aligned16(dh) || !aligned16(gate) || !aligned16(up) ||
+        !aligned16(dgate) || !aligned16(dup) || !aligned4(coef) || !aligned4(n_rows) || !aligned4(dcoef) ||
+        !good_ld(ld_dh, width, e) || !good_ld(ld_gate, width, e) || !good_ld(ld_up, width, e) ||
+        !good_ld(ld_dgate, width, e) || !good_ld(ld_dup, width, e))
+        return MOE_ERR_INVALID_ARG;
+    DevInfo di;
+    const moe_status st = check_device(&di);
+    if (st != MOE_OK) return st;
+    SwigluArgs a;
+    memset(&a, 0, sizeof(a));
+    a.gate = gate;
+    a.up = up;
+    a.dh = dh;
+    a.out0 = dgate;
+    a.out1 = dup;
+    a.coef = coef;
+    a.dcoef = dcoef;
+    a.n_rows = n_rows;
+    a.ld_gate = ld_gate;
+    a.ld_up = ld_up;
+    a.ld_dh = ld_dh;
+    a.ld_out0 = ld_dgate;
+    a.ld_out1 = ld_dup;
+    a.rows = rows;
+    a.width = width;
+    return cuda_status(launch_swiglu(true, dtype, a, di.sm_count, (cudaStream_t)stream));
+}
+
+moe_status moe_quantize_int8(const void* x, moe_dtype dtype, int64_t ldx, int rows, int k, const int32_t* n_rows,
+                             int8_t* q, float* sx, moe_stream_t stream) {
+    NvtxRange nv("moe.quantize_int8");
+    if (!is_float(dtype)) return refused(dtype);
+    if (rows < 0 || rows > kMaxRows || k < 16 || k > kMaxQuantWidth || k % 16 != 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !sx || !aligned16(x) || !aligned16(q) || !aligned4(sx) || !aligned4(n_rows) ||
+        !good_ld(ldx, k, size_of(dtype)))
+        return MOE_ERR_INVALID_ARG;
+    DevInfo di;
+    const moe_status st = check_device(&di);
+    if (st != MOE_OK) return st;
+    return cuda_status(
+        launch_quantize_int8(x, dtype, ldx, rows, k, n_rows, q, sx, di.sm_count, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,655 @@
+// Matrix products grouped by expert with ragged sizes, on CTA pairs.
+//
+// Rows sorted by group; off[g] .. off[g+1] are group g's rows.  Three products:
+//   RAG_NT  y[r, n]     = sum_k x[r, k] w[g(r), n, k]      (w as nn.Linear keeps it)
+//   RAG_NN  y[r, n]     = sum_k x[r, k] w[g(r), k, n]      (the input gradient, same w)
+//   RAG_TN  dw[g, n, k] = sum_{r in g} dy[r, n] x[r, k]    (the weight gradient)
+// in 16-bit types with fp32 sums, and RAG_NT in 8-bit integers with exact 32-bit sums
+// and one scale per row and per output channel.
+//
+// Tiling.  The output's feature axis n is M of the tensor-core tile (256 per CTA
+// pair, 128 per SM), the ragged row axis (TN: the k axis) is N, up to 256 wide.  A
+// group's rows then cost MMA width only in steps of 32, where rows as M would pad
+// every group to 128 or 256 of them.  A group of more than 256 rows is cut into
+// equal chunks.  Each SM loads its own 128 features and half of the chunk's rows.
+// An accumulator is 256 TMEM columns, so two fit: the epilogue of one item overlaps
+// the products of the next.
+//
+// NN and TN read operands whose summed axis is the row axis of memory: their tiles
+// are MN-major in shared memory (64 elements of the free axis by 64 of the summed
+// one per 8 KB block).  TN sums over a group's rows, which end inside a 64-row block:
+// a warp zeroes the rows behind the group's last in both tiles before the MMA may
+// read them (zero in one only would keep a NaN of the next group).
+//
+// Nothing is scheduled on the host: every CTA builds the groups' item counts in
+// shared memory from the offsets and walks the items with the stride of the grid.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "moe_gemm2.cuh"
+
+namespace moe {
+
+constexpr int RAG_STAGE_A = 128 * 128;    // 128 features x 128 bytes of the summed axis
+constexpr int RAG_STAGE_B = 128 * 128;
+constexpr int RAG_STAGE = RAG_STAGE_A + RAG_STAGE_B;
+constexpr int RAG_TN_BLOCK = 64 * 128;    // one 64 x 64 block of an MN-major tile
+// Warps: 0-3 load (one TMA instruction each per stage: a thread issues one every few
+// hundred cycles whatever its size, and a stage of 64 is consumed in about 700),
+// 4 issues the MMAs, 5 zeroes TN's tail rows, 6-13 are the epilogue.
+constexpr int RAG_EPI_WARP0 = 6;
+constexpr int RAG_EPI_WARPS = 8;
+constexpr int RAG_THREADS = (RAG_EPI_WARP0 + RAG_EPI_WARPS) * 32;
+constexpr int RAG_BAND = 8;               // chunks whose items run together (L2)
+
+template <int DIR>
+struct RagCfg {
+    // a staging tile of the epilogue, per warp: 32 rows of 64 (NT, NN) or 128 bytes
+    static constexpr int STAGING = DIR == RAG_TN ? 4096 : 2048;
+    static constexpr int STAGES = DIR == RAG_TN ? 5 : 6;
+    static constexpr int TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;  // first row, rows, first item of each group
+    static constexpr int MISC = 256;
+    static constexpr int SMEM_BYTES = 1024 + STAGES * RAG_STAGE + RAG_EPI_WARPS * STAGING + TABLE + MISC;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
+};
+
+// One unit of work of a CTA pair.
+struct RagItem {
+    int g;        // group
+    int m;        // 256-feature tile
+    int row0;     // first row (TN: the group's first row)
+    int rows;     // rows of the chunk (TN: rows of the group, the summed length)
+    int col0;     // TN: first column of dw
+    int width;    // valid columns of the tile: rows of the chunk (TN: columns of dw)
+    int chunks;   // chunks of the group that read the same weights
+};
+
+
+struct RagTable {
+    int* start;   // [groups] first row
+    int* count;   // [groups] rows
+    int* first;   // [groups + 1] first item
+};
+
+// Items of a group of `rows` rows.
+template <int DIR>
+__device__ __forceinline__ int rag_items_of(const RaggedArgs& P, int rows) {
+    const int mt = (P.n + 255) >> 8;
+    return mt * (DIR == RAG_TN ? (P.k + 255) >> 8 : (rows + 255) >> 8);
+}
+
+// Fills the table from the offsets (all threads of the CTA).  A group whose offsets
+// decrease or leave [0, rows] has no rows and sets MOE_DEVERR_BAD_ROWS.
+template <int DIR>
+__device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTable& t, int* warp_sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (P.groups + RAG_THREADS - 1) / RAG_THREADS;  // consecutive groups of a thread
+    const int g0 = tid * per;
+    int sum = 0;
+    for (int g = g0; g < min(g0 + per, P.groups); ++g) {
+        int a = 0, b = P.rows;
+        if (P.offsets) {
+            a = __ldg(P.offsets + g);
+            b = __ldg(P.offsets + g + 1);
+        }
+        if (a < 0 || b < a || b > P.rows) {
+            if (blockIdx.x == 0) set_dev_error(MOE_DEVERR_BAD_ROWS);
+            a = b = 0;
+        }
+        t.start[g] = a;
+        t.count[g] = b - a;
+        t.first[g] = sum;  // within the thread, for now
+        sum += rag_items_of<DIR>(P, b - a);
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sums[w];
+    for (int g = g0; g < min(g0 + per, P.groups); ++g) t.first[g] += base;
+    if (tid == RAG_THREADS - 1) t.first[P.groups] = base + sum;
+}
+
+// Item i: the group by bisection, then inside it bands of RAG_BAND chunks (TN: column
+// tiles).  A band's chunks run together over the feature tiles, so that at any time the
+// pairs work on a block of about RAG_BAND chunks x 9 tiles whose operands L2 holds.
+template <int DIR>
+__device__ __forceinline__ RagItem rag_item(const RaggedArgs& P, const RagTable& t, int i) {
+    int lo = 0, hi = P.groups - 1;  // largest g with first[g] <= i
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= i) lo = mid;
+        else hi = mid - 1;
+    }
+    RagItem it;
+    it.g = lo;
+    it.row0 = t.start[lo];
+    it.rows = t.count[lo];
+    const int mt = (P.n + 255) >> 8;
+    const int nc = DIR == RAG_TN ? (P.k + 255) >> 8 : (it.rows + 255) >> 8;
+    int local = i - t.first[lo];
+    const int band = local / (RAG_BAND * mt);
+    local -= band * RAG_BAND * mt;
+    const int nb = min(RAG_BAND, nc - band * RAG_BAND);
+    it.m = local / nb;
+    const int c = band * RAG_BAND + local - it.m * nb;
+    it.chunks = nc;
+    if (DIR == RAG_TN) {
+        it.col0 = c * 256;
+        it.width = min(256, P.k - it.col0);
+    } else {
+        const int w = ((it.rows + nc - 1) / nc + 31) & ~31;  // equal chunks, at most 256 rows
+        it.col0 = 0;
+        it.row0 += c * w;
+        it.width = min(w, it.rows - c * w);
+        it.rows = it.width;
+    }
+    return it;
+}
+
+// Blocks of 128 bytes (NT; NN, TN: of 64 rows) of the summed axis an item reads.
+template <int DIR, bool I8>
+__device__ __forceinline__ int rag_blocks(const RaggedArgs& P, const RagItem& it) {
+    if (DIR == RAG_TN) return (it.rows + 63) >> 6;
+    return I8 ? (P.k + 127) >> 7 : (P.k + 63) >> 6;
+}
+
+// Width of the MMA: the item's, in steps of 32 (NT, NN) or of the 64-column blocks of
+// both CTAs (TN; the loads fill columns past dw's last with zeros).
+template <int DIR>
+__device__ __forceinline__ int rag_mma_n(const RagItem& it) {
+    return DIR == RAG_TN ? (it.width + 127) & ~127 : (it.width + 31) & ~31;
+}
+
+// MN-major operand tile in 128-byte-swizzled 64 x 64 blocks: 8 rows of the summed axis
+// are 1024 bytes (stride byte offset), the next 64 elements of the free axis RAG_TN_BLOCK
+// further (leading byte offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(RAG_TN_BLOCK >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Instruction descriptor: kind::f16 (fp32 sums; `fmt` 0 = f16, 1 = bf16) or kind::i8
+// (32-bit sums of signed 8-bit operands); bits 15 / 16 say that A / B is MN-major.
+template <int DIR, bool I8>
+__device__ __forceinline__ uint32_t rag_idesc(uint32_t fmt, uint32_t N) {
+    const uint32_t d_fmt = I8 ? 2u : 1u, ab = I8 ? 1u : fmt;
+    return (d_fmt << 4) | (ab << 7) | (ab << 10) | (DIR != RAG_NT ? 1u << 15 : 0u) | (DIR == RAG_TN ? 1u << 16 : 0u) |
+           ((N >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma2_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 3-D tiled load (x inner, y, z) counted on an mbarrier of either CTA of the pair.  No multicast.
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, int x, int y, int z,
+                                                 uint32_t mbar_cluster, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar_cluster), "l"(policy)
+        : "memory");
+}
+
+// The wait of the MMA issuer for a stage that warps of both CTAs hand over (acquire at
+// cluster scope: the peer's zeroed rows are then visible); else as mbar_wait_bounded.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                          uint64_t limit_ns = 2000000000ull) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > limit_ns) {
+                set_dev_error(MOE_DEVERR_TIMEOUT);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// fp32 -> 16-bit bits, one rounding to nearest even.
+__device__ __forceinline__ uint32_t rag_pack2(float a, float b, int bf16) {
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint16_t rag_pack1(float a, int bf16) { return (uint16_t)(rag_pack2(a, a, bf16) & 0xffffu); }
+__device__ __forceinline__ float rag_unpack(uint16_t v, int bf16) {
+    if (bf16) return __uint_as_float((uint32_t)v << 16);
+    return __half2float(__ushort_as_half(v));
+}
+
+// Epilogue of NT / NN for 32 columns (rows of y) of a warp's 32 features: v[j] is
+// feature f0 + lane of row row0 + j, j < valid.
+// A row of y gets 32 consecutive features from the warp: 128 bytes in fp32, stored as
+// they are; in 16 bits they pass through `stage` so that a lane stores 16 bytes and the
+// warp eight rows' 64-byte pieces with one instruction (two-byte stores: eight times the
+// instructions).  With accumulate the sum is rounded once, so the old value is added to
+// the fp32 one, in place.
+__device__ __forceinline__ void rag_store_rows(const RaggedArgs& P, uint8_t* stage, int row0, int valid, int f0,
+                                               const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    const int f = f0 + lane;
+    if (P.out == MOE_F32) {
+        if (f < P.n) {
+            float* y = static_cast<float*>(P.y) + (size_t)row0 * P.ldy + f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < valid) y[(size_t)j * P.ldy] = P.accumulate ? y[(size_t)j * P.ldy] + v[j] : v[j];
+        }
+        return;
+    }
+    const int bf16 = P.out == MOE_BF16;
+    if (P.accumulate) {
+        if (f < P.n) {
+            uint16_t* y = static_cast<uint16_t*>(P.y) + (size_t)row0 * P.ldy + f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < valid) {
+                    uint16_t* p = y + (size_t)j * P.ldy;
+                    *p = rag_pack1(rag_unpack(*p, bf16) + v[j], bf16);
+                }
+        }
+        return;
+    }
+    uint16_t* st = reinterpret_cast<uint16_t*>(stage);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) st[j * 32 + lane] = rag_pack1(v[j], bf16);
+    __syncwarp();
+    const int part = lane & 3;
+    if (f0 + part * 8 < P.n) {  // n is a multiple of 8: a piece is inside or outside
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i * 8 + (lane >> 2);
+            if (j < valid)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)(row0 + j) * P.ldy + f0 + part * 8) =
+                    *reinterpret_cast<const uint4*>(stage + j * 64 + part * 16);
+        }
+    }
+    __syncwarp();
+}
+
+// Epilogue of TN: lane holds row f0 + lane of dw, columns c0 .. (32 fp32 values, or 64
+// 16-bit ones already packed); the warp's 4 KB tile is staged (16-byte pieces swizzled by
+// the row, free of bank conflicts) and stored as whole 128-byte pieces of rows.
+__device__ __forceinline__ void rag_stage_piece(uint8_t* stage, int piece, uint4 v) {
+    const int lane = threadIdx.x & 31;
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+}
+__device__ __forceinline__ uint4 rag_staged(const uint8_t* stage, int row, int piece) {
+    return *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void rag_store_f32_tile(const RaggedArgs& P, uint8_t* stage, size_t base, int f0, int c0,
+                                                   const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        rag_stage_piece(stage, i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                             __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+    __syncwarp();
+    const int piece = lane & 7, col = c0 + piece * 4;
+    if (col < P.k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (f0 + r >= P.n) continue;
+            const uint4 u = rag_staged(stage, r, piece);
+            float4 s = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                   __uint_as_float(u.w));
+            const size_t at = base + (size_t)(f0 + r) * P.k + col;
+            if (P.out == MOE_F32) {
+                float4* p = reinterpret_cast<float4*>(static_cast<float*>(P.y) + at);
+                if (P.accumulate) {
+                    const float4 o = *p;
+                    s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
+                }
+                *p = s;
+            } else {  // 16-bit accumulate: added in fp32, rounded once
+                const int bf16 = P.out == MOE_BF16;
+                uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.y) + at);
+                const uint2 o = *p;
+                s.x += rag_unpack((uint16_t)o.x, bf16);
+                s.y += rag_unpack((uint16_t)(o.x >> 16), bf16);
+                s.z += rag_unpack((uint16_t)o.y, bf16);
+                s.w += rag_unpack((uint16_t)(o.y >> 16), bf16);
+                *p = make_uint2(rag_pack2(s.x, s.y, bf16), rag_pack2(s.z, s.w, bf16));
+            }
+        }
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void rag_store_h16_tile(const RaggedArgs& P, uint8_t* stage, size_t base, int f0, int c0) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    const int piece = lane & 7, col = c0 + piece * 8;
+    if (col < P.k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (f0 + r < P.n)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + base + (size_t)(f0 + r) * P.k + col) =
+                    rag_staged(stage, r, piece);
+        }
+    }
+    __syncwarp();
+}
+
+template <int DIR, bool I8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
+    moe_ragged_kernel(const __grid_constant__ RaggedArgs P) {
+    using C = RagCfg<DIR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = smem;
+    uint8_t* staging = smem + C::STAGES * RAG_STAGE;
+    RagTable tab;
+    tab.start = reinterpret_cast<int*>(staging + RAG_EPI_WARPS * C::STAGING);
+    tab.count = tab.start + RAG_MAX_GROUPS;
+    tab.first = tab.count + RAG_MAX_GROUPS;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tab.start) + C::TABLE);
+    uint64_t* full = bars;                     // leader: stage ready for the MMA (NT, NN: both CTAs' bytes)
+    uint64_t* empty = bars + C::STAGES;        // both: stage consumed
+    uint64_t* landed = bars + 2 * C::STAGES;   // TN, both: this CTA's bytes of the stage
+    uint64_t* tfull = bars + 3 * C::STAGES;    // [2] both: accumulator written
+    uint64_t* tempty = tfull + 2;              // [2] leader: accumulator read by both epilogues
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* warp_sums = reinterpret_cast<int*>(tmem_slot + 2);  // [RAG_THREADS / 32]
+    static_assert((3 * C::STAGES + 5) * 8 + (2 + RAG_THREADS / 32) * 4 <= C::MISC, "barriers fit");
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], DIR == RAG_TN ? 2 : 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&landed[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * RAG_EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) tmem_alloc_pair(tmem_slot);
+    rag_build_table<DIR>(P, tab, warp_sums);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = tab.first[P.groups];
+    const int cluster_id = blockIdx.x >> 1;
+    const int n_clusters = gridDim.x >> 1;
+
+    if (warp < 4) {
+        // -------------------------------------------------------- loads (both CTAs)
+        // warp 0: A (NN, TN: its first 64 features), 1: A's other 64, 2: B (TN: its
+        // first 64 columns), 3: B's other 64
+        const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT) || (warp == 3 && DIR == RAG_TN);
+        if (works && lane == 0) {
+            const uint64_t pol_stream = l2_policy_evict_first();
+            const uint64_t pol_keep = l2_policy_evict_last();
+            const uint64_t pol_normal = l2_policy_evict_normal();
+            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+            const uint32_t landed0 = mapa_shared(smem_u32(&landed[0]), rank);
+            const int half = (warp & 1) * 64;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int i = cluster_id; i < total; i += n_clusters) {
+                const RagItem it = rag_item<DIR>(P, tab, i);
+                const int blocks = rag_blocks<DIR, I8>(P, it);
+                const int f0 = it.m * 256 + (int)rank * 128;
+                const int nh = rag_mma_n<DIR>(it) / 2;      // this CTA's columns of the tile
+                // weights that one chunk reads stream; those of several chunks stay for the others
+                const uint64_t pol_w = DIR == RAG_TN ? pol_normal : it.chunks > 1 ? pol_keep : pol_stream;
+                // rows of the smallest box that holds this CTA's rows (NT, NN)
+                const int box = nh > 64 ? 128 : nh > 16 ? 64 : 16;
+                const CUtensorMap* bmap = nh > 64 ? &P.b128 : nh > 16 ? &P.b64 : &P.b16;
+                const int n_bbox = nh > 64 ? 2 : 1;          // TN: 64-column blocks
+                const uint32_t bytes = DIR == RAG_TN ? (uint32_t)(RAG_STAGE_A + n_bbox * RAG_TN_BLOCK)
+                                                     : 2u * (uint32_t)(RAG_STAGE_A + box * 128);
+                bool ok = true;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+                    uint8_t* sa = ring + stage * RAG_STAGE;
+                    uint8_t* sb = sa + RAG_STAGE_A;
+                    const uint32_t fb = (DIR == RAG_TN ? landed0 : full0) + (uint32_t)(stage * 8);
+                    if (warp == 0) {
+                        if (DIR == RAG_TN) mbar_arrive_expect_tx(&landed[stage], bytes);
+                        else if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+                    }
+                    if (DIR == RAG_NT) {
+                        if (warp == 0) tma_load_3d_pair(sa, &P.a, kb * (I8 ? 128 : 64), f0, it.g, fb, pol_w);
+                        else tma_load_2d_pair(sb, bmap, kb * (I8 ? 128 : 64), it.row0 + (int)rank * nh, fb, pol_normal);
+                    } else if (DIR == RAG_NN) {
+                        if (warp < 2) tma_load_3d_pair(sa + half * 128, &P.a, f0 + half, kb * 64, it.g, fb, pol_w);
+                        else tma_load_2d_pair(sb, bmap, kb * 64, it.row0 + (int)rank * nh, fb, pol_normal);
+                    } else if (warp < 2) {
+                        tma_load_2d_pair(sa + half * 128, &P.a, f0 + half, it.row0 + kb * 64, fb, pol_normal);
+                    } else if (half == 0 || n_bbox == 2) {
+                        tma_load_2d_pair(sb + half * 128, &P.b64, it.col0 + (int)rank * nh + half, it.row0 + kb * 64,
+                                         fb, pol_normal);
+                    }
+                    if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == 4) {
+        if (lane == 0 && leader) {
+            // ---------------------------------------------------- 2-SM MMA issuer
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t acc_phase = 0;  // bit b: phase of accumulator b
+            int buf = 0;
+            bool issued = false;
+            for (int i = cluster_id; i < total; i += n_clusters) {
+                const RagItem it = rag_item<DIR>(P, tab, i);
+                const int blocks = rag_blocks<DIR, I8>(P, it);
+                if (blocks == 0) continue;  // TN, a group without rows: the epilogue writes zeros
+                const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, (uint32_t)rag_mma_n<DIR>(it));
+                if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+                // elements of the summed axis: the last block ends with it (TN: rows past it are
+                // zero up to a multiple of 16; NT, NN: the loads filled in zeros)
+                const int len = DIR == RAG_TN ? it.rows : P.k;
+                bool ok = true;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    const bool landed_ok = DIR == RAG_TN ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag)
+                                                         : mbar_wait_bounded(&full[stage], phase, abort_flag);
+                    if (!landed_ok) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(ring + stage * RAG_STAGE);
+                    const uint64_t ad = DIR == RAG_NT ? smem_desc_sw128(a_addr) : smem_desc_mn_sw128(a_addr);
+                    const uint64_t bd = DIR == RAG_TN ? smem_desc_mn_sw128(a_addr + RAG_STAGE_A)
+                                                      : smem_desc_sw128(a_addr + RAG_STAGE_A);
+                    // one step sums 32 bytes of a K-major row, or 16 rows (2048 bytes) of an MN-major tile
+                    constexpr uint64_t a_step = DIR == RAG_NT ? 2 : 128, b_step = DIR == RAG_TN ? 128 : 2;
+                    constexpr int per_step = I8 ? 32 : 16;
+                    const int left = len - kb * 4 * per_step;
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        if (s * per_step >= left) break;
+                        const uint32_t accum = (kb > 0 || s != 0) ? 1u : 0u;
+                        if (I8) mma2_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                        else mma2_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                    }
+                    mma2_commit_pair(&empty[stage], 0x3);
+                    issued = true;
+                    if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                mma2_commit_pair(&tfull[buf], 0x3);
+                acc_phase ^= 1u << buf;
+                buf ^= 1;
+            }
+            if (*abort_flag && issued) {
+                mma2_commit_local(drain);
+                volatile int dummy = 0;
+                mbar_wait_bounded(drain, 0, &dummy, 100000000ull);
+            }
+        }
+    } else if (warp == 5) {
+        if (DIR == RAG_TN) {
+            // ---------------------------------------------------- tail rows (both CTAs)
+            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int i = cluster_id; i < total; i += n_clusters) {
+                const RagItem it = rag_item<DIR>(P, tab, i);
+                const int blocks = rag_blocks<DIR, I8>(P, it);
+                bool ok = true;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    int got = 0;
+                    if (lane == 0) got = mbar_wait_bounded(&landed[stage], phase, abort_flag) ? 1 : 0;
+                    got = __shfl_sync(0xffffffffu, got, 0);
+                    if (!got) { ok = false; break; }
+                    const int r0 = it.rows - kb * 64;  // rows of the group in this block
+                    if (r0 < 64 && (r0 & 15)) {
+                        // rows r0 .. the next multiple of 16: a row is 128 bytes of each 64 x 64 block
+                        mbar_wait_bounded(&landed[stage], phase, abort_flag);  // every lane sees the landed bytes
+                        const int n = ((r0 + 15) & ~15) - r0;
+                        uint8_t* st = ring + stage * RAG_STAGE;
+                        for (int j = lane; j < n * 32; j += 32) {
+                            const int row = r0 + (j >> 5), blk = (j >> 3) & 3, piece = j & 7;
+                            *reinterpret_cast<uint4*>(st + blk * RAG_TN_BLOCK + row * 128 + piece * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive_cluster_release(full0 + (uint32_t)(stage * 8));
+                    if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue (both CTAs, own TMEM)
+        const int q = warp & 3;                          // TMEM lane quarter of this warp
+        const int half = (warp - RAG_EPI_WARP0) >> 2;
+        uint8_t* stage = staging + (warp - RAG_EPI_WARP0) * C::STAGING;
+        const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+        uint32_t acc_phase = 0;
+        int buf = 0;
+        for (int i = cluster_id; i < total; i += n_clusters) {
+            const RagItem it = rag_item<DIR>(P, tab, i);
+            const int f0 = it.m * 256 + (int)rank * 128 + q * 32;
+            if (DIR == RAG_TN && it.rows == 0) {
+                if (!P.accumulate && f0 + lane < P.n) {
+                    uint8_t* row = static_cast<uint8_t*>(P.y) +
+                                   (((size_t)it.g * P.n + f0 + lane) * P.k + it.col0) * (P.out == MOE_F32 ? 4 : 2);
+                    const int pieces = it.width * (P.out == MOE_F32 ? 4 : 2) / 16;  // k is a multiple of 8
+                    for (int p = half; p < pieces; p += 2) reinterpret_cast<uint4*>(row)[p] = make_uint4(0, 0, 0, 0);
+                }
+                continue;
+            }
+            float sw = 0.0f;
+            if (I8 && f0 + lane < P.n) sw = __ldg(P.sw + (size_t)it.g * P.n + f0 + lane);
+            int got = 0;
+            if (lane == 0) got = mbar_wait_bounded(&tfull[buf], (acc_phase >> buf) & 1u, abort_flag) ? 1 : 0;
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if (!got) break;
+            tc_fence_after();
+            const uint32_t t0 = tmem_base + (uint32_t)(buf * 256) + ((uint32_t)(q * 32) << 16);
+            if (DIR == RAG_TN) {
+                const size_t base = (size_t)it.g * P.n * P.k;
+                for (int c0 = 64 * half; c0 < it.width; c0 += 128) {
+                    float v[32];
+                    const bool wide = P.out != MOE_F32 && !P.accumulate;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_ld32(t0 + (uint32_t)(c0 + 32 * h), v);
+                        if (wide) {
+                            const int bf16 = P.out == MOE_BF16;
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                rag_stage_piece(stage, 4 * h + p,
+                                                make_uint4(rag_pack2(v[8 * p], v[8 * p + 1], bf16),
+                                                           rag_pack2(v[8 * p + 2], v[8 * p + 3], bf16),
+                                                           rag_pack2(v[8 * p + 4], v[8 * p + 5], bf16),
+                                                           rag_pack2(v[8 * p + 6], v[8 * p + 7], bf16)));
+                        } else {
+                            rag_store_f32_tile(P, stage, base, f0, it.col0 + c0 + 32 * h, v);
+                        }
+                    }
+                    if (wide) rag_store_h16_tile(P, stage, base, f0, it.col0 + c0);
+                }
+            } else {
+                for (int c0 = 32 * half; c0 < it.width; c0 += 64) {
+                    float v[32];
+                    float sx = 0.0f;
+                    if (I8 && c0 + lane < it.width) sx = __ldg(P.sx + it.row0 + c0 + lane);
+                    tmem_ld32(t0 + (uint32_t)c0, v);
+                    if (I8) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = (float)__float_as_int(v[j]) * (__shfl_sync(0xffffffffu, sx, j) * sw);
+                    }
+                    rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, v);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * 8));
+            acc_phase ^= 1u << buf;
+            buf ^= 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while its peer may still signal it
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base);
+    }
+}
+
+}  // namespace moe

@@ -62,7 +62,7 @@ typedef enum {
     MOE_ERR_CUDA = 5           /* a CUDA runtime call or launch failed */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_F16 = 3 } moe_dtype;
 
 /* Device error word bits (moe_device_error). */
 #define MOE_DEVERR_BAD_EXPERT 0x1u    /* a routed expert id outside [0, n_experts) */
@@ -326,6 +326,82 @@ MOE_API moe_status moe_dense_ffn(int d, int hidden, moe_dtype act_dtype, moe_dty
                                  const float* s_down, const void* x, int T, void* y, moe_dtype y_dtype,
                                  int accumulate, void* workspace, size_t ws_bytes, moe_stream_t stream,
                                  const moe_stage_events* events);
+
+/* ---------------------------------------------------------------- products by group
+ * The experts' products as operators of their own, with their gradients, for
+ * training and for 8-bit experts; no counterpart on the pages.  Rows are sorted by
+ * group (expert), as moe_permute and the dispatch leave them: offsets [groups + 1]
+ * int32 on the device, group g holding rows offsets[g] .. offsets[g + 1] - 1 of a
+ * buffer of `rows` rows.  offsets[0] may be above 0 and offsets[groups] below `rows`
+ * (a block of experts, a buffer with room): rows outside are neither read into a
+ * result nor written.  offsets = NULL with groups = 1: all rows.  Groups may be
+ * empty.  A group whose offsets decrease or leave [0, rows] counts as empty and sets
+ * MOE_DEVERR_BAD_ROWS.
+ *   - 1 <= groups <= 1024; rows <= 2^24; n, k multiples of 8 (8-bit operands: k of
+ *     16), at most 65536.
+ *   - ld*: elements from one row to the next, at least the row, a multiple of 16
+ *     bytes; so halves of a wider buffer can be read and written in place.  Weights
+ *     and their gradients are dense.
+ *   - Outputs may not overlap inputs.  One launch, no workspace, results that do
+ *     not depend on the run; sums in fp32 (8-bit operands: exact in 32 bits),
+ *     rounded once.  accumulate = 1 adds to the output, before that rounding. */
+
+/* y[r, :] (+)= x[r, :] . W_g^T for r in group g.  x [rows, k] and w of `dtype`
+ * (MOE_BF16 or MOE_F16); y [rows, n] of the same type or MOE_F32.
+ *   transpose_w = 0: w [groups, n, k], y[r, j] = sum_i x[r, i] w[g, j, i], the
+ *                    projection with nn.Linear's layout;
+ *   transpose_w = 1: w [groups, k, n], y[r, j] = sum_i x[r, i] w[g, i, j], with the
+ *                    same w the gradient of the projection's input. */
+MOE_API moe_status moe_grouped_mm(int groups, int rows, int n, int k, moe_dtype dtype, const void* x, int64_t ldx,
+                                  const void* w, int transpose_w, const int32_t* offsets, void* y, int64_t ldy,
+                                  moe_dtype y_dtype, int accumulate, moe_stream_t stream);
+
+/* dw[g, j, i] (+)= sum over the rows r of group g of dy[r, j] x[r, i]: the gradient
+ * of the projection's weights.  dy [rows, n], x [rows, k] of `dtype` (MOE_BF16 or
+ * MOE_F16); dw [groups, n, k] of the same type or MOE_F32.  An empty group's dw is
+ * zero (accumulate = 1: left as it is), for rows = 0 too. */
+MOE_API moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dtype dtype, const void* dy, int64_t lddy,
+                                     const void* x, int64_t ldx, const int32_t* offsets, void* dw, moe_dtype dw_dtype,
+                                     int accumulate, moe_stream_t stream);
+
+/* SwiGLU of each row with its coefficient (the routing weight, where it is applied
+ * before the down projection):
+ *   h[r, :] = coef[r] * SiLU(gate[r, :]) * up[r, :]        SiLU(z) = z * sigmoid(z)
+ * gate, up, h: [rows, width] of `dtype` (MOE_F32, MOE_BF16 or MOE_F16), width a
+ * multiple of 8, at most 65536; coef [rows] fp32, or NULL for 1; n_rows: device count
+ * of the rows to compute (e.g. offsets + groups; the rows behind are left as they
+ * were; a count outside [0, rows] computes none and sets MOE_DEVERR_BAD_ROWS), or
+ * NULL for all.  Computed in fp32, rounded once.  h may be gate or up itself. */
+MOE_API moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* gate, int64_t ld_gate, const void* up,
+                              int64_t ld_up, const float* coef, const int32_t* n_rows, void* h, int64_t ld_h,
+                              moe_stream_t stream);
+
+/* The gradients of moe_swiglu from dh: with s = sigmoid(gate), a = gate * s
+ *   dgate = coef * dh * up * (s + a * (1 - s)),  dup = coef * dh * a,
+ *   dcoef[r] = sum over the row of dh * a * up     fp32 [rows], or NULL
+ * dgate may be gate and dup may be up (or dh) itself.  The sum has a fixed order. */
+MOE_API moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, const void* dh, int64_t ld_dh,
+                                       const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                                       const float* coef, const int32_t* n_rows, void* dgate, int64_t ld_dgate,
+                                       void* dup, int64_t ld_dup, float* dcoef, moe_stream_t stream);
+
+/* 8-bit codes with one scale per row (activations per token; a weight matrix's rows
+ * are its output channels, so the same call quantises weights):
+ *   sx[r]   = max |x[r, :]| / 127, or 1 where that is zero    fp32 [rows]
+ *   q[r, c] = the integer nearest to the real quotient x[r, c] / sx[r], ties to even,
+ *             in [-127, 127]                                  int8 [rows, k]
+ * x: [rows, k] MOE_F32, MOE_BF16 or MOE_F16, k a multiple of 16, at most 32768.  A
+ * row with an infinity or a NaN gets codes 0 and a scale that is not finite, so that
+ * its products are NaN.  n_rows as in moe_swiglu. */
+MOE_API moe_status moe_quantize_int8(const void* x, moe_dtype dtype, int64_t ldx, int rows, int k,
+                                     const int32_t* n_rows, int8_t* q, float* sx, moe_stream_t stream);
+
+/* y[r, j] (+)= sx[r] * sw[g, j] * sum_i q[r, i] w[g, j, i] for r in group g, the sum
+ * exact.  q [rows, k] and w [groups, n, k] int8, sx [rows], sw [groups, n] fp32; y
+ * [rows, n] MOE_F32, MOE_BF16 or MOE_F16.  A dense layer is one group. */
+MOE_API moe_status moe_grouped_mm_int8(int groups, int rows, int n, int k, const int8_t* q, const float* sx,
+                                       const int8_t* w, const float* sw, const int32_t* offsets, void* y, int64_t ldy,
+                                       moe_dtype y_dtype, int accumulate, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- expert parallelism
  * The routed experts split over n_ranks ranks (one process per GPU) in

@@ -1,0 +1,526 @@
+"""The products grouped by expert, SwiGLU with its gradient and the int8 codes on a B200, against plain 64-bit
+arithmetic.
+
+Tolerances.  Products of two 16-bit values are exact in fp32; a sum of m terms in fp32 with additions off by at
+most one unit of 2^-23 of the running magnitude is off by at most m 2^-23 sum |x w| (_sum_bound).  A result in a
+type t is then off by half a step more, eps(t) / 2 of its value (fp32 results: that is inside the sum's bound).
+Integer sums are exact; the fp32 conversion and the two scales are three roundings."""
+import numpy as np
+import pytest
+import torch
+
+import fine_grained_moe_gemm_b200 as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, FH, FS = torch.bfloat16, torch.float16, torch.float32
+
+# rows of the groups: empty ones, one row, around 16, 32, 64 and 256, several chunks
+RAGGED = [0, 1, 0, 15, 16, 17, 33, 0, 64, 65, 255, 256, 257, 0, 530, 0]
+FEW = [3, 0, 1, 7]
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _rand(gen, shape, dtype, std=1.0):
+    return (torch.randn(shape, generator=gen, device=DEV) * std).to(dtype)
+
+
+def _wide(t, pad=24):
+    """The same matrix as a slice of a wider buffer whose other values are NaN."""
+    buf = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=DEV)
+    v = buf[:, 8:8 + t.shape[1]]
+    v.copy_(t)
+    return v
+
+
+def _offsets(sizes, first=0):
+    return torch.tensor(np.concatenate([[first], first + np.cumsum(sizes)]), dtype=torch.int32, device=DEV)
+
+
+def _eps(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def _within(got, ref, bound, what="result"):
+    got = got.double()
+    bad = ~((got - ref).abs() <= bound)
+    if bool(bad.any()):
+        worst = float((got - ref).abs().nan_to_num(1e30).max())
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} outside, worst error {worst}, first at "
+                             f"{bad.nonzero()[0].tolist()}")
+
+
+def _mm_ref(x, w, sizes, first, transpose):
+    """Reference and its sum of magnitudes, rows of the groups only."""
+    ref, mag, a = [], [], first
+    for g, m in enumerate(sizes):
+        xs, ws = x[a:a + m].double(), w[g].double() if transpose else w[g].double().t()
+        ref.append(xs @ ws)
+        mag.append(xs.abs() @ ws.abs())
+        a += m
+    return torch.cat(ref), torch.cat(mag)
+
+
+def _mm_case(sizes, n, k, dtype, out, transpose, seed=0, first=0, spare=0, strided=False, accumulate=False):
+    gen = _gen(seed)
+    rows, end = first + sum(sizes) + spare, first + sum(sizes)
+    x = _rand(gen, (rows, k), dtype)
+    x[:first] = float("nan")           # rows outside the groups must not matter
+    x[end:] = float("nan")
+    w = _rand(gen, (len(sizes), k, n) if transpose else (len(sizes), n, k), dtype, 0.1)
+    old = _rand(gen, (rows, n), out)
+    y = _wide(old) if strided else old.clone()
+    if strided:
+        x = _wide(x)
+    moe.moe_grouped_mm(x, w, _offsets(sizes, first), y, transpose_w=transpose, accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert moe.device_error() == 0
+    ref, mag = _mm_ref(x, w, sizes, first, transpose)
+    bound = (k + 2) * 2.0 ** -23 * mag
+    if accumulate:
+        ref = ref + old[first:end].double()
+        bound = bound + 2.0 ** -23 * old[first:end].double().abs()
+    if out != FS:
+        bound = bound * (1 + _eps(out)) + _eps(out) * ref.abs()
+        if out == FH:
+            bound = bound + 2.0 ** -25     # half a step of the subnormal numbers
+    _within(y[first:end], ref, bound)
+    assert torch.equal(y[:first], old[:first]) and torch.equal(y[end:], old[end:])
+    if strided:
+        whole = y.as_strided((rows, n + 24), (n + 24, 1), 0)
+        assert bool(whole[:, :8].isnan().all()) and bool(whole[:, 8 + n:].isnan().all())
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("n,k", [(8, 8), (64, 64), (136, 72), (264, 1160), (512, 256), (1032, 200)])
+@pytest.mark.parametrize("sizes", [FEW, RAGGED])
+def test_mm_sizes(sizes, n, k, transpose):
+    _mm_case(sizes, n, k, BF, FS, transpose, seed=n + k)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, FS), (FH, FH), (FH, FS)])
+def test_mm_types(dtype, out, accumulate, strided, transpose):
+    _mm_case(RAGGED, 152, 328, dtype, out, transpose, seed=7, first=5, spare=9, strided=strided, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("sizes", [[1], [5], [300], [0, 0, 0, 1000], [1] * 300, [0] * 1023 + [2], [2049, 0, 1]])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_mm_groups(sizes, transpose):
+    _mm_case(sizes, 256, 128, BF, BF, transpose, seed=len(sizes))
+
+
+def test_mm_without_offsets_and_without_rows():
+    gen = _gen(3)
+    x, w = _rand(gen, (77, 96), BF), _rand(gen, (1, 40, 96), BF)
+    y = torch.empty((77, 40), dtype=FS, device=DEV)
+    moe.moe_grouped_mm(x, w, None, y)
+    ref, mag = _mm_ref(x, w, [77], 0, False)
+    _within(y, ref, 98 * 2.0 ** -23 * mag)
+    moe.moe_grouped_mm(x[:0], w, None, y[:0])
+    assert moe.device_error() == 0
+
+
+def _wgrad_case(sizes, n, k, dtype, out, seed=0, first=0, spare=0, strided=False, accumulate=False, poison=None):
+    gen = _gen(seed)
+    rows, end = first + sum(sizes) + spare, first + sum(sizes)
+    dy, x = _rand(gen, (rows, n), dtype), _rand(gen, (rows, k), dtype)
+    for t in (dy, x):
+        t[:first] = float("nan")
+        t[end:] = float("nan")
+    starts = np.concatenate([[first], first + np.cumsum(sizes)])
+    if poison is not None:
+        dy[starts[poison]:starts[poison + 1]] = float("nan")
+        x[starts[poison]:starts[poison + 1]] = float("inf")
+    if strided:
+        dy, x = _wide(dy), _wide(x)
+    old = _rand(gen, (len(sizes), n, k), out)
+    dw = old.clone()
+    moe.moe_grouped_wgrad(dy, x, _offsets(sizes, first), dw, accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert moe.device_error() == 0
+    for g, m in enumerate(sizes):
+        if g == poison:
+            assert m == 0 or bool(dw[g].isnan().all())
+            continue
+        a, b = dy[starts[g]:starts[g + 1]].double(), x[starts[g]:starts[g + 1]].double()
+        ref, bound = a.t() @ b, (m + 2) * 2.0 ** -23 * (a.abs().t() @ b.abs())
+        if accumulate:
+            ref, bound = ref + old[g].double(), bound + 2.0 ** -23 * old[g].double().abs()
+        if out != FS:
+            bound = bound * (1 + _eps(out)) + _eps(out) * ref.abs() + (2.0 ** -25 if out == FH else 0.0)
+        if m == 0:
+            assert torch.equal(dw[g], old[g] if accumulate else torch.zeros_like(old[g]))
+        _within(dw[g], ref, bound, f"group {g} of {m} rows")
+
+
+@pytest.mark.parametrize("n,k", [(8, 8), (64, 64), (136, 72), (264, 520), (512, 256), (1032, 200)])
+@pytest.mark.parametrize("sizes", [FEW, RAGGED])
+def test_wgrad_sizes(sizes, n, k):
+    _wgrad_case(sizes, n, k, BF, FS, seed=n + k)
+
+
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, FS), (FH, FH), (FH, FS)])
+def test_wgrad_types(dtype, out, accumulate, strided):
+    _wgrad_case(RAGGED, 152, 328, dtype, out, seed=11, first=3, spare=70, strided=strided, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("poison", [3, 9, 11])
+def test_wgrad_neighbours_do_not_leak(poison):
+    """A group of NaN and infinities lies right behind another group's last rows, inside its 64-row block."""
+    _wgrad_case(RAGGED, 136, 136, BF, FS, seed=12, poison=poison)
+
+
+def test_wgrad_without_rows_is_zero():
+    dw = torch.full((3, 16, 24), float("nan"), device=DEV)
+    none = torch.empty((0, 16), dtype=BF, device=DEV), torch.empty((0, 24), dtype=BF, device=DEV)
+    moe.moe_grouped_wgrad(*none, _offsets([0, 0, 0]), dw)
+    assert bool((dw == 0).all())
+    dw.fill_(2.0)
+    moe.moe_grouped_wgrad(*none, _offsets([0, 0, 0]), dw, accumulate=True)
+    assert bool((dw == 2.0).all())
+
+
+@pytest.mark.parametrize("bad,g_bad", [([0, 5, 3, 3], 1), ([-1, 5, 6, 9], 0), ([0, 5, 6, 11], 2)])
+def test_bad_offsets_are_empty_groups(bad, g_bad):
+    """One of three groups decreases, starts below zero or ends behind the ten rows; the others are computed."""
+    gen = _gen(5)
+    off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+    x, w = _rand(gen, (10, 32), BF), _rand(gen, (3, 16, 32), BF)
+    dy = _rand(gen, (10, 16), BF)
+    y = torch.full((10, 16), 7.0, device=DEV)
+    dw = torch.full((3, 16, 32), 7.0, device=DEV)
+    moe.moe_grouped_mm(x, w, off, y)
+    assert moe.device_error() == moe.MOE_DEVERR_BAD_ROWS
+    moe.moe_grouped_wgrad(dy, x, off, dw)
+    assert moe.device_error() == moe.MOE_DEVERR_BAD_ROWS
+    covered = torch.zeros(10, dtype=torch.bool, device=DEV)
+    for g in range(3):
+        a, b = bad[g], bad[g + 1]
+        if g == g_bad:
+            assert bool((dw[g] == 0).all())
+            continue
+        covered[a:b] = True
+        xs, ds = x[a:b].double(), dy[a:b].double()
+        _within(dw[g], ds.t() @ xs, 12 * 2.0 ** -23 * (ds.abs().t() @ xs.abs()))
+        _within(y[a:b], xs @ w[g].double().t(), 34 * 2.0 ** -23 * (xs.abs() @ w[g].double().abs().t()))
+    assert bool((y[~covered] == 7.0).all())
+
+
+# ------------------------------------------------------------------ int8
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+@pytest.mark.parametrize("rows,k", [(1, 16), (3, 48), (7, 512), (130, 7168), (2, 18432), (5, 32768), (4000, 80)])
+def test_int8_codes(rows, k, dtype):
+    gen = _gen(k)
+    x = _rand(gen, (rows, k), dtype)
+    x[0] = 0.0
+    if rows > 2:
+        # quotients on the border: x = (c + 1/2) s exactly, with s a power of two
+        x[1] = ((torch.arange(k, device=DEV) % 254 - 127).float() + 0.5).clamp(-126.5, 126.5).to(dtype)
+        x[1, 0] = 127.0
+        x[2] = x[2] * 2.0 ** (-120 if dtype != FH else -14)
+    if rows > 4:
+        x[3, k // 2] = float("inf")
+        x[4, k - 1] = float("nan")
+    x = _wide(x) if rows % 2 else x
+    q = torch.full((rows, k), 99, dtype=torch.int8, device=DEV)
+    sx = torch.full((rows,), -1.0, device=DEV)
+    moe.moe_quantize_int8(x, q, sx)
+    bad = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    if rows > 4:
+        bad[3] = bad[4] = True
+        assert bool((q[3:5] == 0).all()) and not bool(sx[3:5].isfinite().any())
+    ref_s = (x.double().abs().amax(1) / 127.0).float()
+    ref_s = torch.where(ref_s == 0, torch.ones_like(ref_s), ref_s)
+    assert torch.equal(sx[~bad], ref_s[~bad])
+    ref_q = torch.round(x.double() / ref_s.double()[:, None]).clamp(-127, 127)
+    assert torch.equal(q[~bad].double(), ref_q[~bad])
+
+
+def test_int8_codes_next_to_the_border():
+    """fp32 values one ulp around every border of a scale that is no power of two."""
+    s = np.float32(0.1234567)
+    amax = np.float32(s * np.float32(127.0))
+    s = np.float32(amax / np.float32(127.0))
+    mid = ((np.arange(-127, 127) + 0.5) * np.float64(s)).astype(np.float32)
+    x = np.concatenate([mid, np.nextafter(mid, np.float32(np.inf)), np.nextafter(mid, np.float32(-np.inf))])
+    x = np.concatenate([[amax], x, np.zeros((-len(x) - 1) % 16, np.float32)]).astype(np.float32)
+    t = torch.from_numpy(x)[None].to(DEV)
+    q, sx = torch.empty(t.shape, dtype=torch.int8, device=DEV), torch.empty(1, device=DEV)
+    moe.moe_quantize_int8(t, q, sx)
+    assert float(sx) == float(s)
+    assert np.array_equal(q.cpu().numpy()[0], np.rint(x.astype(np.float64) / np.float64(s)))
+
+
+def _codes(gen, shape):
+    return torch.randint(-128, 128, shape, generator=gen, device=DEV, dtype=torch.int32).to(torch.int8)
+
+
+@pytest.mark.parametrize("out", [BF, FH, FS])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("sizes,n,k", [(FEW, 8, 16), (RAGGED, 136, 80), (RAGGED, 264, 1168), ([16], 1032, 2064),
+                                       ([300], 256, 128), ([0] * 200 + [1], 64, 32), ([2], 16, 65536)])
+def test_mm_int8(sizes, n, k, accumulate, out):
+    gen = _gen(n + k)
+    first, spare = (0, 0) if len(sizes) == 1 else (4, 6)
+    rows, end = first + sum(sizes) + spare, first + sum(sizes)
+    q, w = _codes(gen, (rows, k)), _codes(gen, (len(sizes), n, k))
+    if sizes == [2]:   # the largest sums: 65536 products of 128 * 128
+        q.fill_(-128)
+        w.fill_(-128)
+    sx = torch.rand(rows, generator=gen, device=DEV) * 1e-3 + 1e-4
+    sw = torch.rand((len(sizes), n), generator=gen, device=DEV) * 1e-2 + 1e-3
+    old = _rand(gen, (rows, n), out)
+    y = old.clone()
+    moe.moe_grouped_mm_int8(q, sx, w, sw, _offsets(sizes, first) if len(sizes) > 1 else None, y, accumulate=accumulate)
+    assert moe.device_error() == 0
+    ref, a = [], first
+    for g, m in enumerate(sizes):
+        acc = q[a:a + m].double() @ w[g].double().t()
+        ref.append(acc * sx[a:a + m].double()[:, None] * sw[g].double())
+        a += m
+    ref = torch.cat(ref)
+    bound = 3.01 * 2.0 ** -24 * ref.abs()
+    if accumulate:
+        ref, o = ref + old[first:end].double(), old[first:end].double().abs()
+        bound = bound + 2.0 ** -24 * (ref.abs() + bound)
+    bound = bound * (1 + _eps(out)) + _eps(out) * ref.abs() + (2.0 ** -25 if out == FH else 0.0)
+    _within(y[first:end], ref, bound)
+    assert torch.equal(y[:first], old[:first]) and torch.equal(y[end:], old[end:])
+
+
+# ------------------------------------------------------------------ SwiGLU
+def _swiglu_ref(gate, up, coef, dh=None):
+    a, b = gate.double(), up.double()
+    c = coef.double()[:, None] if coef is not None else 1.0
+    s = torch.sigmoid(a)
+    h = c * a * s * b
+    if dh is None:
+        return h
+    d = dh.double()
+    return h, c * d * b * s * (1 + a * (1 - s)), c * d * a * s, (d * a * s * b)
+
+
+def _swiglu_bound(out, size):
+    """fp32 steps: the exponential and the quotients are good to 2^-21 (fast forms: |a| 2^-24 in the exponent's
+    argument as well, |a| < 16 where the value matters), four more roundings; `size` bounds the terms."""
+    return 2.0 ** -18 * size + _eps(out) * size * 1.01 + (2.0 ** -24 if out == FH else 1e-30)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+@pytest.mark.parametrize("rows,width", [(1, 8), (3, 24), (5, 128), (257, 200), (33, 2048), (300, 18432 // 8), (2, 65536)])
+@pytest.mark.parametrize("with_coef", [False, True])
+def test_swiglu(rows, width, dtype, with_coef):
+    gen = _gen(rows + width)
+    gate, up, dh = (_rand(gen, (rows, width), dtype, s) for s in (2.0, 1.0, 0.5))
+    gate[0, 0], gate[0, 1], gate[0, 2], gate[0, 3] = -100.0, 100.0, 0.0, -20.0
+    coef = torch.rand(rows, generator=gen, device=DEV) if with_coef else None
+    if rows > 2 and with_coef:
+        coef[1] = 0.0
+    gate, up = _wide(gate), _wide(up)
+    h = torch.empty((rows, width), dtype=dtype, device=DEV)
+    dgate, dup = _wide(torch.zeros_like(h)), torch.empty_like(h)
+    dcoef = torch.empty(rows, device=DEV) if with_coef else None
+    moe.moe_swiglu(gate, up, h, coef=coef)
+    moe.moe_swiglu_backward(dh, gate, up, dgate, dup, coef=coef, dcoef=dcoef)
+    rh, rg, ru, dots = _swiglu_ref(gate, up, coef, dh)
+    _within(h, rh, _swiglu_bound(dtype, rh.abs()))
+    a, c = gate.double(), coef.double()[:, None] if with_coef else 1.0
+    s = torch.sigmoid(a)
+    # the terms s and a s (1 - s) of dgate may cancel: their magnitudes bound the error
+    _within(dgate, rg, _swiglu_bound(dtype, rg.abs()) + 2.0 ** -18 * (c * dh.double() * up.double()).abs() * (s + (a * s * (1 - s)).abs()))
+    _within(dup, ru, _swiglu_bound(dtype, ru.abs()))
+    if with_coef:
+        _within(dcoef, dots.sum(1), (2.0 ** -18 + (width + 32) * 2.0 ** -24) * dots.abs().sum(1) + 1e-30)
+    # in place: the gradients over gate and up, and over dh
+    g2, u2, d2 = gate.clone(), up.clone(), dh.clone()
+    moe.moe_swiglu_backward(d2, g2, u2, g2, u2, coef=coef)
+    assert torch.equal(g2, dgate) and torch.equal(u2, dup)
+    g2 = gate.clone()
+    moe.moe_swiglu_backward(d2, g2, up, g2, d2, coef=coef)
+    assert torch.equal(g2, dgate) and torch.equal(d2, dup)
+    g2 = gate.clone()
+    moe.moe_swiglu(g2, up, g2, coef=coef)
+    assert torch.equal(g2, h)
+
+
+def test_swiglu_against_differences():
+    gen = _gen(17)
+    gate, up, dh = (_rand(gen, (6, 40), FS, s) for s in (1.5, 1.0, 1.0))
+    coef = torch.rand(6, generator=gen, device=DEV) + 0.5
+    dg, du, dc = torch.empty_like(gate), torch.empty_like(gate), torch.empty_like(coef)
+    moe.moe_swiglu_backward(dh, gate, up, dg, du, coef=coef, dcoef=dc)
+    step = 2.0 ** -6
+
+    def f(g, u, c):
+        h = torch.empty_like(g)
+        moe.moe_swiglu(g, u, h, coef=c)
+        return h.double() * dh.double()
+
+    # central difference: step^2 / 6 of the third derivative (of SiLU: below 1 everywhere) and the forward's
+    # fp32 error (2^-20 of values below 64) over the step
+    scale = (dh * coef[:, None]).double().abs()
+    tol = (step ** 2 / 6 * up.double().abs() + 2.0 ** -20 * 64 / step) * scale + 1e-6
+    _within(dg, (f(gate + step, up, coef) - f(gate - step, up, coef)) / (2 * step), tol)
+    _within(du, (f(gate, up + step, coef) - f(gate, up - step, coef)) / (2 * step), 2.0 ** -20 * 64 / step * scale + 1e-6)
+    _within(dc, ((f(gate, up, coef + step) - f(gate, up, coef - step)) / (2 * step)).sum(1),
+            40 * 2.0 ** -20 * 64 / step * dh.double().abs().amax(1) + 1e-6)
+
+
+@pytest.mark.parametrize("count", [0, 1, 5, 12])
+def test_rows_behind_the_count_stay(count):
+    gen = _gen(count)
+    gate, up, dh = (_rand(gen, (12, 64), BF) for _ in range(3))
+    n = torch.tensor([0, count], dtype=torch.int32, device=DEV)[1:]
+    h, dg, du = (torch.full((12, 64), 3.0, dtype=BF, device=DEV) for _ in range(3))
+    dc, coef = torch.full((12,), 3.0, device=DEV), torch.ones(12, device=DEV)
+    q, sx = torch.full((12, 64), 3, dtype=torch.int8, device=DEV), torch.full((12,), 3.0, device=DEV)
+    moe.moe_swiglu(gate, up, h, coef=coef, n_rows=n)
+    moe.moe_swiglu_backward(dh, gate, up, dg, du, coef=coef, dcoef=dc, n_rows=n)
+    moe.moe_quantize_int8(gate, q, sx, n_rows=n)
+    assert moe.device_error() == 0
+    for t in (h, dg, du, dc, q, sx):
+        assert bool((t[count:] == 3).all())
+    full = torch.empty_like(h)
+    moe.moe_swiglu(gate, up, full, coef=coef)
+    assert torch.equal(h[:count], full[:count])
+    n.fill_(13)
+    moe.moe_swiglu(gate, up, h, n_rows=n)
+    assert moe.device_error() == moe.MOE_DEVERR_BAD_ROWS
+
+
+# ------------------------------------------------------------------ together
+def _ffn(sizes, d, hid, seed=0):
+    gen = _gen(seed)
+    G, R = len(sizes), sum(sizes)
+    t = {"x": _rand(gen, (R, d), BF), "dy": _rand(gen, (R, d), BF), "off": _offsets(sizes),
+         "coef": torch.rand(R, generator=gen, device=DEV),
+         "wg": _rand(gen, (G, hid, d), BF, d ** -0.5), "wu": _rand(gen, (G, hid, d), BF, d ** -0.5),
+         "wd": _rand(gen, (G, d, hid), BF, hid ** -0.5)}
+    gu = torch.empty((R, 2 * hid), dtype=BF, device=DEV)
+    dgu = torch.empty_like(gu)
+    t["gate"], t["up"], t["dgate"], t["dup"] = gu[:, :hid], gu[:, hid:], dgu[:, :hid], dgu[:, hid:]
+    t["h"], t["dh"] = torch.empty((R, hid), dtype=BF, device=DEV), torch.empty((R, hid), dtype=BF, device=DEV)
+    t["y"], t["dx"] = torch.empty((R, d), device=DEV), torch.empty((R, d), device=DEV)
+    t["dcoef"] = torch.empty(R, device=DEV)
+    for n in ("wg", "wu", "wd"):
+        t["d" + n] = torch.empty(t[n].shape, device=DEV)
+    return t
+
+
+def _ffn_step(t, stream=None):
+    o, kw = t["off"], {"stream": stream}
+    moe.moe_grouped_mm(t["x"], t["wg"], o, t["gate"], **kw)
+    moe.moe_grouped_mm(t["x"], t["wu"], o, t["up"], **kw)
+    moe.moe_swiglu(t["gate"], t["up"], t["h"], coef=t["coef"], **kw)
+    moe.moe_grouped_mm(t["h"], t["wd"], o, t["y"], **kw)
+    moe.moe_grouped_wgrad(t["dy"], t["h"], o, t["dwd"], **kw)
+    moe.moe_grouped_mm(t["dy"], t["wd"], o, t["dh"], transpose_w=True, **kw)
+    moe.moe_swiglu_backward(t["dh"], t["gate"], t["up"], t["dgate"], t["dup"], coef=t["coef"], dcoef=t["dcoef"], **kw)
+    moe.moe_grouped_wgrad(t["dgate"], t["x"], o, t["dwg"], **kw)
+    moe.moe_grouped_wgrad(t["dup"], t["x"], o, t["dwu"], **kw)
+    moe.moe_grouped_mm(t["dgate"], t["wg"], o, t["dx"], transpose_w=True, **kw)
+    moe.moe_grouped_mm(t["dup"], t["wu"], o, t["dx"], transpose_w=True, accumulate=True, **kw)
+
+
+_FFN_OUT = ("y", "dx", "dcoef", "dwg", "dwu", "dwd")
+
+
+def test_expert_ffn_forward_and_backward():
+    """The experts' FFN as a training step runs it, against autograd in 64 bits on the unrounded chain.  Each of the
+    two or three bf16 intermediates on a path is off by 2^-8 of its value; as independent relative errors of
+    2^-8 / sqrt(3) each, their effect on a sum stays below 3 x 2^-8 of its root mean square."""
+    sizes = [0, 40, 1, 130, 300, 0, 7]
+    t = _ffn(sizes, 256, 136)
+    _ffn_step(t)
+    torch.cuda.synchronize()
+    assert moe.device_error() == 0
+    leaf = {n: t[n].double().requires_grad_() for n in ("x", "coef", "wg", "wu", "wd")}
+    off = t["off"].tolist()
+    ys = []
+    for g in range(len(sizes)):
+        s = slice(off[g], off[g + 1])
+        a, b = leaf["x"][s] @ leaf["wg"][g].t(), leaf["x"][s] @ leaf["wu"][g].t()
+        ys.append((leaf["coef"][s, None] * torch.nn.functional.silu(a) * b) @ leaf["wd"][g].t())
+    y = torch.cat(ys)
+    y.backward(t["dy"].double())
+    ref = {"y": y.detach(), "dx": leaf["x"].grad, "dcoef": leaf["coef"].grad, "dwg": leaf["wg"].grad,
+           "dwu": leaf["wu"].grad, "dwd": leaf["wd"].grad}
+    for n in _FFN_OUT:
+        err = (t[n].double() - ref[n]).square().mean().sqrt()
+        assert float(err) <= 3 * 2.0 ** -8 * float(ref[n].square().mean().sqrt()), n
+
+
+def test_ffn_captured_replayed_and_on_other_streams():
+    sizes = [5, 0, 260, 33, 1]
+    t, other = _ffn(sizes, 128, 64, seed=1), _ffn(sizes, 128, 64, seed=2)
+    _ffn_step(t)
+    _ffn_step(other)
+    torch.cuda.synchronize()
+    want = [t[n].clone() for n in _FFN_OUT], [other[n].clone() for n in _FFN_OUT]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    graphs = []
+    for v, s in ((t, s1), (other, s2)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            _ffn_step(v, stream=s)
+        graphs.append(g)
+    for v in (t, other):
+        for n in _FFN_OUT:
+            v[n].fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(3):                    # both graphs at once: no buffer is shared
+        with torch.cuda.stream(s1):
+            graphs[0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for v, w in zip((t, other), want):
+        for n, r in zip(_FFN_OUT, w):
+            assert torch.equal(v[n], r), n   # bit for bit: no atomics, fixed orders
+    # new routing in the captured buffers is picked up: everything in the last group
+    t["off"].copy_(_offsets([0, 0, 0, 0, sum(sizes)]))
+    with torch.cuda.stream(s1):
+        graphs[0].replay()
+    torch.cuda.synchronize()
+    fresh = _ffn(sizes, 128, 64, seed=1)
+    fresh["off"] = t["off"]
+    _ffn_step(fresh)
+    for n in _FFN_OUT:
+        assert torch.equal(t[n], fresh[n]), n
+    assert moe.device_error() == 0
+
+
+def test_int8_ffn_against_the_bf16_one():
+    """The experts in 8 bits: weights per output channel, activations per row, both products.  A code is off by half
+    a step of amax / 127; for normal values amax is about 4 standard deviations at these lengths, so one operand's
+    relative error is 4 / 127 / sqrt(12) < 1 %; four operands and SwiGLU stay below 5 % of the output's size."""
+    sizes = [3, 90, 0, 20]
+    t = _ffn(sizes, 256, 128, seed=4)
+    R, d, hid, G = sum(sizes), 256, 128, len(sizes)
+
+    def codes(w):
+        q, s = torch.empty(w.shape, dtype=torch.int8, device=DEV), torch.empty(w.shape[:-1], device=DEV)
+        moe.moe_quantize_int8(w.reshape(-1, w.shape[-1]), q.view(-1, w.shape[-1]), s.view(-1))
+        return q, s
+
+    xq, xs = codes(t["x"])
+    for w, y in (("wg", "gate"), ("wu", "up")):
+        wq, ws = codes(t[w])
+        moe.moe_grouped_mm_int8(xq, xs, wq, ws, t["off"], t[y])
+    moe.moe_swiglu(t["gate"], t["up"], t["h"], coef=t["coef"])
+    hq, hs = codes(t["h"])
+    wq, ws = codes(t["wd"])
+    moe.moe_grouped_mm_int8(hq, hs, wq, ws, t["off"], t["y"])
+    got = t["y"].double()
+    _ffn_step(t)
+    err = (got - t["y"].double()).square().mean().sqrt()
+    assert float(err) <= 0.05 * float(t["y"].double().square().mean().sqrt())
+    assert moe.device_error() == 0

@@ -1,0 +1,137 @@
+"""The products grouped by expert and the row operators on the host: what the C ABI refuses before it touches a
+device, and what the binding refuses before it calls."""
+import ctypes
+
+import pytest
+import torch
+
+import fine_grained_moe_gemm_b200 as moe
+
+P = ctypes.c_void_p
+BAD, UNS, OK = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_OK
+B16, H16, F32, E43 = moe.MOE_BF16, moe.MOE_F16, moe.MOE_F32, moe.MOE_E4M3
+NO_GPU = not torch.cuda.is_available()
+
+
+def _mm(groups=4, rows=10, n=64, k=32, dtype=B16, x=16, ldx=32, w=16, tr=0, off=16, y=16, ldy=64, out=B16, acc=0):
+    p = lambda v: None if v is None else P(v)
+    return moe.lib().moe_grouped_mm(groups, rows, n, k, dtype, p(x), ldx, p(w), tr, p(off), p(y), ldy, out, acc, None)
+
+
+SHAPES = [dict(groups=0), dict(groups=1025), dict(rows=-1), dict(rows=(1 << 24) + 1), dict(n=0), dict(n=12), dict(k=4),
+          dict(k=36), dict(n=65544), dict(k=65544), dict(off=None), dict(off=18), dict(acc=2), dict(out=17)]
+
+
+@pytest.mark.parametrize("wrong", SHAPES + [
+    dict(x=None), dict(w=None), dict(y=None), dict(x=24), dict(w=8), dict(y=4), dict(ldx=31), dict(ldx=36), dict(ldy=56),
+    dict(ldy=68), dict(tr=2), dict(dtype=9), dict(ldy=66, out=F32)])
+def test_mm_refuses(wrong):
+    assert _mm(**wrong) == BAD
+
+
+def test_mm_types_and_nothing_to_do():
+    assert _mm(dtype=F32, out=F32) == UNS and _mm(dtype=E43) == UNS
+    assert _mm(dtype=B16, out=H16) == UNS and _mm(dtype=H16, out=B16) == UNS
+    assert _mm(out=E43) == BAD
+    assert _mm(rows=0, x=None, w=None, y=None) == OK
+    if NO_GPU:
+        assert _mm() == UNS and _mm(groups=1, off=None) == UNS
+
+
+def _wgrad(groups=4, rows=10, n=64, k=32, dtype=B16, dy=16, lddy=64, x=16, ldx=32, off=16, dw=16, out=F32, acc=0):
+    p = lambda v: None if v is None else P(v)
+    return moe.lib().moe_grouped_wgrad(groups, rows, n, k, dtype, p(dy), lddy, p(x), ldx, p(off), p(dw), out, acc, None)
+
+
+@pytest.mark.parametrize("wrong", SHAPES + [dict(dy=None), dict(x=None), dict(dw=None), dict(dy=8), dict(dw=8),
+                                            dict(lddy=60), dict(ldx=33), dict(rows=0, dw=None)])
+def test_wgrad_refuses(wrong):
+    assert _wgrad(**wrong) == BAD
+
+
+def test_wgrad_types():
+    assert _wgrad(dtype=F32) == UNS and _wgrad(dtype=H16, out=B16) == UNS
+    if NO_GPU:
+        assert _wgrad() == UNS and _wgrad(rows=0, dy=None, x=None) == UNS
+
+
+def _mm8(groups=4, rows=10, n=64, k=32, q=16, sx=4, w=16, sw=4, off=16, y=16, ldy=64, out=B16, acc=0):
+    p = lambda v: None if v is None else P(v)
+    return moe.lib().moe_grouped_mm_int8(groups, rows, n, k, p(q), p(sx), p(w), p(sw), p(off), p(y), ldy, out, acc, None)
+
+
+@pytest.mark.parametrize("wrong", SHAPES + [dict(k=8), dict(k=24), dict(q=None), dict(sx=None), dict(w=None),
+                                            dict(sw=None), dict(y=None), dict(q=8), dict(sx=2), dict(ldy=60),
+                                            dict(out=E43)])
+def test_mm_int8_refuses(wrong):
+    assert _mm8(**wrong) == BAD
+
+
+def test_mm_int8_accepts():
+    assert _mm8(rows=0, q=None, sx=None, w=None, sw=None, y=None) == OK
+    if NO_GPU:
+        for out in (B16, H16, F32):
+            assert _mm8(out=out) == UNS
+
+
+def _swiglu(rows=4, width=64, dtype=B16, gate=16, ldg=64, up=16, ldu=64, coef=None, n=None, h=16, ldh=64):
+    p = lambda v: None if v is None else P(v)
+    return moe.lib().moe_swiglu(rows, width, dtype, p(gate), ldg, p(up), ldu, p(coef), p(n), p(h), ldh, None)
+
+
+def _swiglu_b(rows=4, width=64, dtype=B16, dh=16, gate=16, up=16, coef=None, n=None, dgate=16, dup=16, dcoef=None, ld=64):
+    p = lambda v: None if v is None else P(v)
+    return moe.lib().moe_swiglu_backward(rows, width, dtype, p(dh), ld, p(gate), ld, p(up), ld, p(coef), p(n), p(dgate), ld,
+                                         p(dup), ld, p(dcoef), None)
+
+
+@pytest.mark.parametrize("wrong", [dict(rows=-1), dict(rows=(1 << 24) + 1), dict(width=0), dict(width=12),
+                                   dict(width=65544), dict(dtype=9), dict(gate=None), dict(up=8), dict(coef=2),
+                                   dict(n=2)])
+def test_swiglu_refuses(wrong):
+    assert _swiglu(**wrong) == BAD
+    assert _swiglu_b(**wrong) == BAD
+
+
+def test_swiglu_more():
+    assert _swiglu(h=None) == BAD and _swiglu(ldg=56) == BAD and _swiglu(ldh=68) == BAD and _swiglu(dtype=E43) == UNS
+    assert _swiglu_b(dh=None) == BAD and _swiglu_b(dgate=8) == BAD and _swiglu_b(dup=None) == BAD
+    assert _swiglu_b(dcoef=2) == BAD and _swiglu_b(ld=60) == BAD and _swiglu_b(dtype=E43) == UNS
+    assert _swiglu(rows=0, gate=None, up=None, h=None) == OK
+    assert _swiglu_b(rows=0, dh=None, gate=None, up=None, dgate=None, dup=None) == OK
+    if NO_GPU:
+        assert _swiglu() == UNS and _swiglu(dtype=F32) == UNS and _swiglu_b(coef=16, dcoef=16) == UNS
+
+
+def _quant(x=16, dtype=B16, ldx=64, rows=4, k=64, n=None, q=16, sx=16):
+    p = lambda v: None if v is None else P(v)
+    return moe.lib().moe_quantize_int8(p(x), dtype, ldx, rows, k, p(n), p(q), p(sx), None)
+
+
+@pytest.mark.parametrize("wrong", [dict(x=None), dict(q=None), dict(sx=None), dict(x=8), dict(q=8), dict(sx=2), dict(n=2),
+                                   dict(rows=-1), dict(k=8), dict(k=72), dict(k=32784), dict(ldx=60), dict(dtype=9)])
+def test_quantize_refuses(wrong):
+    assert _quant(**wrong) == BAD
+
+
+def test_quantize_more():
+    assert _quant(dtype=E43) == UNS and _quant(rows=0, x=None, q=None, sx=None) == OK
+    if NO_GPU:
+        assert _quant() == UNS
+
+
+def test_binding_refuses_host_tensors():
+    x, w, y = torch.zeros(4, 16).bfloat16(), torch.zeros(2, 8, 16).bfloat16(), torch.zeros(4, 8)
+    off = torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: moe.moe_grouped_mm(x, w, off, y), lambda: moe.moe_grouped_wgrad(x, x, off, w),
+                 lambda: moe.moe_swiglu(x, x, x), lambda: moe.moe_swiglu_backward(x, x, x, x, x),
+                 lambda: moe.moe_quantize_int8(x, x.to(torch.int8), y[:, 0]),
+                 lambda: moe.moe_grouped_mm_int8(x.to(torch.int8), y[:, 0], w.to(torch.int8), y[:2], off, y)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_enum_matches_the_header():
+    text = open(moe.HEADER_PATH).read()
+    assert "MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_F16 = 3" in text
+    assert (moe.MOE_F32, moe.MOE_BF16, moe.MOE_E4M3, moe.MOE_F16) == (0, 1, 2, 3)
