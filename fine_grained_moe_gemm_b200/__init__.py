@@ -755,8 +755,8 @@ def moe_swiglu_backward(dh, gate, up, dgate, dup, coef=None, dcoef=None, n_rows=
 
 
 def moe_quantize_int8(x, q, sx, n_rows=None, stream=None):
-    """int8 codes q [R, k] and fp32 scales sx [R] of the rows of x [R, k] (fp32, bf16 or f16): sx = max|x| / 127, q the
-    nearest integer of x / sx, ties to even.  Weights [.., n, k] quantise per output channel through a view of
+    """int8 codes q [R, k] and fp32 scales sx [R] of the rows of x [R, k] (fp32, bf16 or f16): sx = max|x| * fp32(1/127),
+    q the nearest integer of x / sx, ties to even.  Weights [.., n, k] quantise per output channel through a view of
     their rows."""
     R, k = x.shape
     ldx = _rows(x, "x", (R, k), tuple(_FLOATS))

@@ -1377,30 +1377,44 @@ cudaError_t launch_ep_combine(const float* back, const int32_t* send_tok, int n_
     return cudaGetLastError();
 }
 
-template <int DIR, bool I8>
+template <int DIR, bool I8, bool PROMOTE>
 static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_t s) {
     constexpr int smem = RagCfg<DIR>::SMEM_BYTES;
+    auto kernel = moe_ragged_kernel<DIR, I8, PROMOTE>;
     static std::atomic<bool> attr_set[64];  // once per device (a repeated set is harmless)
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
-        cudaError_t e = cudaFuncSetAttribute(moe_ragged_kernel<DIR, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             smem);
+        if (PROMOTE) {  // the warps share out the registers of the launch: they must be there
+            cudaFuncAttributes fa;
+            cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs < RAG_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+        }
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
     }
     note_launch();
-    moe_ragged_kernel<DIR, I8><<<grid, RAG_THREADS, smem, s>>>(*args);
+    kernel<<<grid, RAG_THREADS, smem, s>>>(*args);
     return cudaGetLastError();
 }
 
 cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s) {
     grid &= ~1;
     if (grid < 2) return cudaErrorInvalidValue;
-    if (i8) return dir == RAG_NT ? launch_ragged_t<RAG_NT, true>(args, grid, s) : cudaErrorInvalidValue;
-    if (dir == RAG_NT) return launch_ragged_t<RAG_NT, false>(args, grid, s);
-    if (dir == RAG_NN) return launch_ragged_t<RAG_NN, false>(args, grid, s);
-    return dir == RAG_TN ? launch_ragged_t<RAG_TN, false>(args, grid, s) : cudaErrorInvalidValue;
+    if (i8) return dir == RAG_NT ? launch_ragged_t<RAG_NT, true, false>(args, grid, s) : cudaErrorInvalidValue;
+    // fp32 results of sums that may be longer than a segment
+    const bool promote = args->out == MOE_F32 && (dir == RAG_TN ? args->rows : args->k) > RAG_SEGMENT;
+    if (dir == RAG_NT)
+        return promote ? launch_ragged_t<RAG_NT, false, true>(args, grid, s)
+                       : launch_ragged_t<RAG_NT, false, false>(args, grid, s);
+    if (dir == RAG_NN)
+        return promote ? launch_ragged_t<RAG_NN, false, true>(args, grid, s)
+                       : launch_ragged_t<RAG_NN, false, false>(args, grid, s);
+    if (dir != RAG_TN) return cudaErrorInvalidValue;
+    return promote ? launch_ragged_t<RAG_TN, false, true>(args, grid, s)
+                   : launch_ragged_t<RAG_TN, false, false>(args, grid, s);
 }
 
 template <typename T>

@@ -31,26 +31,40 @@
 
 namespace moe {
 
-constexpr int RAG_STAGE_A = 128 * 128;    // 128 features x 128 bytes of the summed axis
-constexpr int RAG_STAGE_B = 128 * 128;
-constexpr int RAG_STAGE = RAG_STAGE_A + RAG_STAGE_B;
+constexpr int RAG_SLOT = 128 * 128;       // one slot of a ring: 128 features (rows) x 128 bytes of the summed axis
 constexpr int RAG_TN_BLOCK = 64 * 128;    // one 64 x 64 block of an MN-major tile
-// Warps: 0-3 load (one TMA instruction each per stage: a thread issues one every few
-// hundred cycles whatever its size, and a stage of 64 is consumed in about 700),
-// 4 issues the MMAs, 5 zeroes TN's tail rows, 6-13 are the epilogue.
-constexpr int RAG_EPI_WARP0 = 6;
+// Warps: 0-3 load (a thread issues one TMA instruction every few hundred cycles whatever
+// its size, and a block of 64 is consumed in about 700), 4 issues the MMAs, 5 zeroes
+// TN's tail rows, 8-15 are the epilogue (6 and 7 fill up their warpgroup).
+constexpr int RAG_EPI_WARP0 = 8;
 constexpr int RAG_EPI_WARPS = 8;
 constexpr int RAG_THREADS = (RAG_EPI_WARP0 + RAG_EPI_WARPS) * 32;
 constexpr int RAG_BAND = 8;               // chunks whose items run together (L2)
+
+// The tensor core cuts each partial sum off instead of rounding it, so a sum of m terms
+// comes out small by about m * 1e-9 of its value (measured: 2.3e-7 at 256 terms, 1.5e-4
+// at 131072).  A 16-bit result does not see that; an fp32 one does.  With PROMOTE the
+// tensor core sums RAG_SEGMENT terms at a time and the epilogue adds the segments in
+// fp32 registers, rounding to nearest.
+constexpr int RAG_SEGMENT = 512;
+// The segments' sums take 128 registers of an epilogue thread, so PROMOTE moves
+// registers from warps 0-7 to warps 8-15: 256 x 56 + 256 x 200 = 512 x 128, the
+// registers that the CTA was launched with (launch_ragged checks that it was).
+constexpr int RAG_REGS_LAUNCH = 128, RAG_REGS_CONTROL = 56, RAG_REGS_EPILOGUE = 200;
 
 template <int DIR>
 struct RagCfg {
     // a staging tile of the epilogue, per warp: 32 rows of 64 (NT, NN) or 128 bytes
     static constexpr int STAGING = DIR == RAG_TN ? 4096 : 2048;
-    static constexpr int STAGES = DIR == RAG_TN ? 5 : 6;
+    // Separate rings: the weights come from HBM and want many bytes under way, the rows
+    // from L2.  TN reads both operands from L2.
+    static constexpr int STAGES_A = DIR == RAG_TN ? 5 : 8;
+    static constexpr int STAGES_B = DIR == RAG_TN ? 5 : 4;
+    static constexpr int RING = (STAGES_A + STAGES_B) * RAG_SLOT;
     static constexpr int TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;  // first row, rows, first item of each group
-    static constexpr int MISC = 256;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * RAG_STAGE + RAG_EPI_WARPS * STAGING + TABLE + MISC;
+    static constexpr int BARS = 2 * (STAGES_A + STAGES_B) + (DIR == RAG_TN ? 2 * STAGES_A + STAGES_B : 0) + 5;
+    static constexpr int MISC = (BARS * 8 + (2 + RAG_THREADS / 32) * 4 + 15) / 16 * 16;
+    static constexpr int SMEM_BYTES = 1024 + RING + RAG_EPI_WARPS * STAGING + TABLE + MISC;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -256,29 +270,47 @@ __device__ __forceinline__ float rag_unpack(uint16_t v, int bf16) {
 }
 
 // Epilogue of NT / NN for 32 columns (rows of y) of a warp's 32 features: v[j] is
-// feature f0 + lane of row row0 + j, j < valid.
-// A row of y gets 32 consecutive features from the warp: 128 bytes in fp32, stored as
-// they are; in 16 bits they pass through `stage` so that a lane stores 16 bytes and the
-// warp eight rows' 64-byte pieces with one instruction (two-byte stores: eight times the
-// instructions).  With accumulate the sum is rounded once, so the old value is added to
-// the fp32 one, in place.
+// feature f0 + lane of row row0 + j, j < valid.  The values pass through the warp's
+// 2 KB of `stage`, so that a lane stores 16 bytes and the warp several rows' pieces (64
+// bytes in 16 bits, 128 in fp32) with one instruction.
+__device__ __forceinline__ void rag_store_rows_f32(const RaggedArgs& P, uint8_t* stage, int row0, int valid, int f0,
+                                                   const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    const int f = f0 + (lane & 7) * 4;  // n is a multiple of 8: a piece is inside or outside
+    float* st = reinterpret_cast<float*>(stage);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {       // 16 rows at a time
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st[j * 32 + lane] = v[16 * h + j];
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const int j = i * 4 + (lane >> 3);
+            if (16 * h + j < valid && f < P.n) {
+                float4 s = *reinterpret_cast<const float4*>(st + j * 32 + (lane & 7) * 4);
+                float4* y = reinterpret_cast<float4*>(static_cast<float*>(P.y) + (size_t)(row0 + 16 * h + j) * P.ldy + f);
+                if (P.accumulate) {
+                    const float4 o = *y;
+                    s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
+                }
+                *y = s;
+            }
+        }
+        __syncwarp();
+    }
+}
+
 __device__ __forceinline__ void rag_store_rows(const RaggedArgs& P, uint8_t* stage, int row0, int valid, int f0,
                                                const float (&v)[32]) {
     const int lane = threadIdx.x & 31;
-    const int f = f0 + lane;
+    const int bf16 = P.out == MOE_BF16;
     if (P.out == MOE_F32) {
-        if (f < P.n) {
-            float* y = static_cast<float*>(P.y) + (size_t)row0 * P.ldy + f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < valid) y[(size_t)j * P.ldy] = P.accumulate ? y[(size_t)j * P.ldy] + v[j] : v[j];
-        }
+        rag_store_rows_f32(P, stage, row0, valid, f0, v);
         return;
     }
-    const int bf16 = P.out == MOE_BF16;
-    if (P.accumulate) {
-        if (f < P.n) {
-            uint16_t* y = static_cast<uint16_t*>(P.y) + (size_t)row0 * P.ldy + f;
+    if (P.accumulate) {  // added in fp32 and rounded once: in place, two bytes a lane
+        if (f0 + lane < P.n) {
+            uint16_t* y = static_cast<uint16_t*>(P.y) + (size_t)row0 * P.ldy + f0 + lane;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 if (j < valid) {
@@ -293,7 +325,7 @@ __device__ __forceinline__ void rag_store_rows(const RaggedArgs& P, uint8_t* sta
     for (int j = 0; j < 32; ++j) st[j * 32 + lane] = rag_pack1(v[j], bf16);
     __syncwarp();
     const int part = lane & 3;
-    if (f0 + part * 8 < P.n) {  // n is a multiple of 8: a piece is inside or outside
+    if (f0 + part * 8 < P.n) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int j = i * 8 + (lane >> 2);
@@ -316,6 +348,7 @@ __device__ __forceinline__ uint4 rag_staged(const uint8_t* stage, int row, int p
     return *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
+template <bool F32>
 __device__ __forceinline__ void rag_store_f32_tile(const RaggedArgs& P, uint8_t* stage, size_t base, int f0, int c0,
                                                    const float (&v)[32]) {
     const int lane = threadIdx.x & 31;
@@ -326,15 +359,15 @@ __device__ __forceinline__ void rag_store_f32_tile(const RaggedArgs& P, uint8_t*
     __syncwarp();
     const int piece = lane & 7, col = c0 + piece * 4;
     if (col < P.k) {
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
-            if (f0 + r >= P.n) continue;
+            if (f0 + r >= P.n) break;
             const uint4 u = rag_staged(stage, r, piece);
             float4 s = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
                                    __uint_as_float(u.w));
             const size_t at = base + (size_t)(f0 + r) * P.k + col;
-            if (P.out == MOE_F32) {
+            if (F32) {
                 float4* p = reinterpret_cast<float4*>(static_cast<float*>(P.y) + at);
                 if (P.accumulate) {
                     const float4 o = *p;
@@ -372,29 +405,65 @@ __device__ __forceinline__ void rag_store_h16_tile(const RaggedArgs& P, uint8_t*
     __syncwarp();
 }
 
-template <int DIR, bool I8>
+// A position in a ring of N slots.
+template <int N>
+struct RagCursor {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    __device__ __forceinline__ void skip(int n) {  // n >= 0
+        const int at = slot + n;
+        phase ^= (uint32_t)((at / N) & 1);
+        slot = at % N;
+    }
+};
+
+// (a0, a1) += (b0, b1), in place and in order: the volatile keeps the next TMEM load
+// behind it, whose registers would come on top of the sums'.
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+    asm volatile(
+        "{\n\t.reg .b64 pa, pb;\n\t"
+        "mov.b64 pa, {%0, %1};\n\t"
+        "mov.b64 pb, {%2, %3};\n\t"
+        "add.rn.f32x2 pa, pa, pb;\n\t"
+        "mov.b64 {%0, %1}, pa;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+
+template <int DIR, bool I8, bool PROMOTE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
     moe_ragged_kernel(const __grid_constant__ RaggedArgs P) {
     using C = RagCfg<DIR>;
+    constexpr int SA = C::STAGES_A, SB = C::STAGES_B;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring = smem;
-    uint8_t* staging = smem + C::STAGES * RAG_STAGE;
+    uint8_t* ring_a = smem;
+    uint8_t* ring_b = smem + SA * RAG_SLOT;
+    uint8_t* staging = smem + C::RING;
     RagTable tab;
     tab.start = reinterpret_cast<int*>(staging + RAG_EPI_WARPS * C::STAGING);
     tab.count = tab.start + RAG_MAX_GROUPS;
     tab.first = tab.count + RAG_MAX_GROUPS;
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tab.start) + C::TABLE);
-    uint64_t* full = bars;                     // leader: stage ready for the MMA (NT, NN: both CTAs' bytes)
-    uint64_t* empty = bars + C::STAGES;        // both: stage consumed
-    uint64_t* landed = bars + 2 * C::STAGES;   // TN, both: this CTA's bytes of the stage
-    uint64_t* tfull = bars + 3 * C::STAGES;    // [2] both: accumulator written
-    uint64_t* tempty = tfull + 2;              // [2] leader: accumulator read by both epilogues
+    uint64_t* full_a = bars;               // leader: both CTAs' bytes of the slot are there
+    uint64_t* full_b = full_a + SA;
+    uint64_t* empty_a = full_b + SB;       // both: slot consumed
+    uint64_t* empty_b = empty_a + SA;
+    uint64_t* tfull = empty_b + SB;        // [2] both: accumulator written
+    uint64_t* tempty = tfull + 2;          // [2] leader: accumulator read by both epilogues
     uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* landed_a = drain + 1;        // TN, blocks with tail rows, both: this CTA's bytes
+    uint64_t* landed_b = landed_a + SA;
+    uint64_t* peer_done = landed_b + SB;   // TN, blocks with tail rows, leader: the peer's tail is zeroed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* warp_sums = reinterpret_cast<int*>(tmem_slot + 2);  // [RAG_THREADS / 32]
-    static_assert((3 * C::STAGES + 5) * 8 + (2 + RAG_THREADS / 32) * 4 <= C::MISC, "barriers fit");
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -402,16 +471,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
     const bool leader = rank == 0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], DIR == RAG_TN ? 2 : 1);
-            mbar_init(&empty[s], 1);
-            mbar_init(&landed[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 2 * RAG_EPI_WARPS);
-        }
-        mbar_init(drain, 1);
+        for (int b = 0; b < C::BARS; ++b) mbar_init(&bars[b], 1);
+        // the two accumulators are released by every epilogue warp of both CTAs
+        for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], 2 * RAG_EPI_WARPS);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -425,181 +487,256 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
     const int total = tab.first[P.groups];
     const int cluster_id = blockIdx.x >> 1;
     const int n_clusters = gridDim.x >> 1;
+    constexpr int seg_blocks = RAG_SEGMENT / (I8 ? 128 : 64);
 
-    if (warp < 4) {
-        // -------------------------------------------------------- loads (both CTAs)
-        // warp 0: A (NN, TN: its first 64 features), 1: A's other 64, 2: B (TN: its
-        // first 64 columns), 3: B's other 64
-        const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT) || (warp == 3 && DIR == RAG_TN);
-        if (works && lane == 0) {
-            const uint64_t pol_stream = l2_policy_evict_first();
-            const uint64_t pol_keep = l2_policy_evict_last();
-            const uint64_t pol_normal = l2_policy_evict_normal();
-            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
-            const uint32_t landed0 = mapa_shared(smem_u32(&landed[0]), rank);
-            const int half = (warp & 1) * 64;
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int i = cluster_id; i < total; i += n_clusters) {
-                const RagItem it = rag_item<DIR>(P, tab, i);
-                const int blocks = rag_blocks<DIR, I8>(P, it);
-                const int f0 = it.m * 256 + (int)rank * 128;
-                const int nh = rag_mma_n<DIR>(it) / 2;      // this CTA's columns of the tile
-                // weights that one chunk reads stream; those of several chunks stay for the others
-                const uint64_t pol_w = DIR == RAG_TN ? pol_normal : it.chunks > 1 ? pol_keep : pol_stream;
-                // rows of the smallest box that holds this CTA's rows (NT, NN)
-                const int box = nh > 64 ? 128 : nh > 16 ? 64 : 16;
-                const CUtensorMap* bmap = nh > 64 ? &P.b128 : nh > 16 ? &P.b64 : &P.b16;
-                const int n_bbox = nh > 64 ? 2 : 1;          // TN: 64-column blocks
-                const uint32_t bytes = DIR == RAG_TN ? (uint32_t)(RAG_STAGE_A + n_bbox * RAG_TN_BLOCK)
-                                                     : 2u * (uint32_t)(RAG_STAGE_A + box * 128);
-                bool ok = true;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-                    uint8_t* sa = ring + stage * RAG_STAGE;
-                    uint8_t* sb = sa + RAG_STAGE_A;
-                    const uint32_t fb = (DIR == RAG_TN ? landed0 : full0) + (uint32_t)(stage * 8);
-                    if (warp == 0) {
-                        if (DIR == RAG_TN) mbar_arrive_expect_tx(&landed[stage], bytes);
-                        else if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-                    }
-                    if (DIR == RAG_NT) {
-                        if (warp == 0) tma_load_3d_pair(sa, &P.a, kb * (I8 ? 128 : 64), f0, it.g, fb, pol_w);
-                        else tma_load_2d_pair(sb, bmap, kb * (I8 ? 128 : 64), it.row0 + (int)rank * nh, fb, pol_normal);
-                    } else if (DIR == RAG_NN) {
-                        if (warp < 2) tma_load_3d_pair(sa + half * 128, &P.a, f0 + half, kb * 64, it.g, fb, pol_w);
-                        else tma_load_2d_pair(sb, bmap, kb * 64, it.row0 + (int)rank * nh, fb, pol_normal);
-                    } else if (warp < 2) {
-                        tma_load_2d_pair(sa + half * 128, &P.a, f0 + half, it.row0 + kb * 64, fb, pol_normal);
-                    } else if (half == 0 || n_bbox == 2) {
-                        tma_load_2d_pair(sb + half * 128, &P.b64, it.col0 + (int)rank * nh + half, it.row0 + kb * 64,
-                                         fb, pol_normal);
-                    }
-                    if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
-                }
-                if (!ok) break;
-            }
-        }
-    } else if (warp == 4) {
-        if (lane == 0 && leader) {
-            // ---------------------------------------------------- 2-SM MMA issuer
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t acc_phase = 0;  // bit b: phase of accumulator b
-            int buf = 0;
-            bool issued = false;
-            for (int i = cluster_id; i < total; i += n_clusters) {
-                const RagItem it = rag_item<DIR>(P, tab, i);
-                const int blocks = rag_blocks<DIR, I8>(P, it);
-                if (blocks == 0) continue;  // TN, a group without rows: the epilogue writes zeros
-                const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, (uint32_t)rag_mma_n<DIR>(it));
-                if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * 256);
-                // elements of the summed axis: the last block ends with it (TN: rows past it are
-                // zero up to a multiple of 16; NT, NN: the loads filled in zeros)
-                const int len = DIR == RAG_TN ? it.rows : P.k;
-                bool ok = true;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    const bool landed_ok = DIR == RAG_TN ? mbar_wait_bounded_cluster(&full[stage], phase, abort_flag)
-                                                         : mbar_wait_bounded(&full[stage], phase, abort_flag);
-                    if (!landed_ok) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a_addr = smem_u32(ring + stage * RAG_STAGE);
-                    const uint64_t ad = DIR == RAG_NT ? smem_desc_sw128(a_addr) : smem_desc_mn_sw128(a_addr);
-                    const uint64_t bd = DIR == RAG_TN ? smem_desc_mn_sw128(a_addr + RAG_STAGE_A)
-                                                      : smem_desc_sw128(a_addr + RAG_STAGE_A);
-                    // one step sums 32 bytes of a K-major row, or 16 rows (2048 bytes) of an MN-major tile
-                    constexpr uint64_t a_step = DIR == RAG_NT ? 2 : 128, b_step = DIR == RAG_TN ? 128 : 2;
-                    constexpr int per_step = I8 ? 32 : 16;
-                    const int left = len - kb * 4 * per_step;
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        if (s * per_step >= left) break;
-                        const uint32_t accum = (kb > 0 || s != 0) ? 1u : 0u;
-                        if (I8) mma2_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
-                        else mma2_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
-                    }
-                    mma2_commit_pair(&empty[stage], 0x3);
-                    issued = true;
-                    if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
-                }
-                if (!ok) break;
-                mma2_commit_pair(&tfull[buf], 0x3);
-                acc_phase ^= 1u << buf;
-                buf ^= 1;
-            }
-            if (*abort_flag && issued) {
-                mma2_commit_local(drain);
-                volatile int dummy = 0;
-                mbar_wait_bounded(drain, 0, &dummy, 100000000ull);
-            }
-        }
-    } else if (warp == 5) {
-        if (DIR == RAG_TN) {
-            // ---------------------------------------------------- tail rows (both CTAs)
-            const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
-            int stage = 0;
-            uint32_t phase = 0;
-            for (int i = cluster_id; i < total; i += n_clusters) {
-                const RagItem it = rag_item<DIR>(P, tab, i);
-                const int blocks = rag_blocks<DIR, I8>(P, it);
-                bool ok = true;
-                for (int kb = 0; kb < blocks; ++kb) {
-                    int got = 0;
-                    if (lane == 0) got = mbar_wait_bounded(&landed[stage], phase, abort_flag) ? 1 : 0;
-                    got = __shfl_sync(0xffffffffu, got, 0);
-                    if (!got) { ok = false; break; }
-                    const int r0 = it.rows - kb * 64;  // rows of the group in this block
-                    if (r0 < 64 && (r0 & 15)) {
-                        // rows r0 .. the next multiple of 16: a row is 128 bytes of each 64 x 64 block
-                        mbar_wait_bounded(&landed[stage], phase, abort_flag);  // every lane sees the landed bytes
-                        const int n = ((r0 + 15) & ~15) - r0;
-                        uint8_t* st = ring + stage * RAG_STAGE;
-                        for (int j = lane; j < n * 32; j += 32) {
-                            const int row = r0 + (j >> 5), blk = (j >> 3) & 3, piece = j & 7;
-                            *reinterpret_cast<uint4*>(st + blk * RAG_TN_BLOCK + row * 128 + piece * 16) =
-                                make_uint4(0, 0, 0, 0);
+    if (warp < RAG_EPI_WARP0) {
+        if (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RAG_REGS_CONTROL));
+        if (warp < 4) {
+            // ---------------------------------------------------- loads (both CTAs)
+            // warp 0: A (NN, TN: its first 64 features), 1: A's other 64, 2: B (TN: its
+            // first 64 columns), 3: B's other 64
+            const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT) || (warp == 3 && DIR == RAG_TN);
+            if (works && lane == 0) {
+                const bool is_a = warp < 2;
+                const int half = (warp & 1) * 64;
+                const uint64_t pol_stream = l2_policy_evict_first();
+                const uint64_t pol_keep = l2_policy_evict_last();
+                const uint64_t pol_normal = l2_policy_evict_normal();
+                uint64_t* full = is_a ? full_a : full_b;
+                uint64_t* empty = is_a ? empty_a : empty_b;
+                uint64_t* landed = is_a ? landed_a : landed_b;
+                uint8_t* ring = is_a ? ring_a : ring_b;
+                const int n_slots = is_a ? SA : SB;
+                const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+                const uint32_t landed0 = mapa_shared(smem_u32(landed), rank);
+                int slot = 0;
+                uint32_t phase = 0;
+                for (int i = cluster_id; i < total; i += n_clusters) {
+                    const RagItem it = rag_item<DIR>(P, tab, i);
+                    const int blocks = rag_blocks<DIR, I8>(P, it);
+                    const int f0 = it.m * 256 + (int)rank * 128;
+                    const int nh = rag_mma_n<DIR>(it) / 2;  // this CTA's columns of the tile
+                    // weights that one chunk reads stream; those of several chunks stay for the others
+                    const uint64_t policy = DIR == RAG_TN || !is_a ? pol_normal : it.chunks > 1 ? pol_keep : pol_stream;
+                    // rows of the smallest box that holds this CTA's rows (NT, NN)
+                    const int box = nh > 64 ? 128 : nh > 16 ? 64 : 16;
+                    const CUtensorMap* bmap = nh > 64 ? &P.b128 : nh > 16 ? &P.b64 : &P.b16;
+                    const bool second = nh > 64;                 // TN: B has a second 64-column block
+                    const uint32_t bytes = is_a ? (uint32_t)RAG_SLOT
+                                           : DIR == RAG_TN ? (second ? 2u : 1u) * RAG_TN_BLOCK : (uint32_t)box * 128u;
+                    const int brow = it.row0 + (int)rank * nh;
+                    bool ok = true;
+                    for (int kb = 0; kb < blocks; ++kb) {
+                        if (!mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag)) { ok = false; break; }
+                        uint8_t* dst = ring + slot * RAG_SLOT + half * 128;
+                        // a block whose last rows belong to the next group is counted where it lies,
+                        // for the warp that zeroes them; the others on the leader's barrier
+                        const bool tail = DIR == RAG_TN && kb == blocks - 1 && (it.rows & 15);
+                        const uint32_t bar = (tail ? landed0 : full0) + (uint32_t)(slot * 8);
+                        if (half == 0) {
+                            if (tail) mbar_arrive_expect_tx(&landed[slot], bytes);
+                            else if (leader) mbar_arrive_expect_tx(&full[slot], 2u * bytes);
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
+                        if (DIR == RAG_TN) {
+                            if (is_a) tma_load_2d_pair(dst, &P.a, f0 + half, it.row0 + kb * 64, bar, policy);
+                            else if (half == 0 || second)
+                                tma_load_2d_pair(dst, &P.b64, it.col0 + (int)rank * nh + half, it.row0 + kb * 64, bar,
+                                                 policy);
+                        } else if (!is_a) {
+                            tma_load_2d_pair(dst, bmap, kb * (I8 ? 128 : 64), brow, bar, policy);
+                        } else if (DIR == RAG_NT) {
+                            tma_load_3d_pair(dst, &P.a, kb * (I8 ? 128 : 64), f0, it.g, bar, policy);
+                        } else {
+                            tma_load_3d_pair(dst, &P.a, f0 + half, kb * 64, it.g, bar, policy);
+                        }
+                        if (++slot == n_slots) { slot = 0; phase ^= 1u; }
                     }
-                    if (lane == 0) mbar_arrive_cluster_release(full0 + (uint32_t)(stage * 8));
-                    if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+                    if (!ok) break;
                 }
-                if (!ok) break;
+            }
+        } else if (warp == 4) {
+            if (lane == 0 && leader) {
+                // ------------------------------------------------ 2-SM MMA issuer
+                RagCursor<SA> ca;
+                RagCursor<SB> cb;
+                uint32_t acc_phase = 0;  // bit b: phase of accumulator b
+                int buf = 0;
+                bool issued = false;
+                for (int i = cluster_id; i < total; i += n_clusters) {
+                    const RagItem it = rag_item<DIR>(P, tab, i);
+                    const int blocks = rag_blocks<DIR, I8>(P, it);
+                    // elements of the summed axis: the last block ends with it (TN: rows past it are
+                    // zero up to a multiple of 16; NT, NN: the loads filled in zeros)
+                    const int len = DIR == RAG_TN ? it.rows : P.k;
+                    const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, (uint32_t)rag_mma_n<DIR>(it));
+                    bool ok = true;
+                    for (int kb = 0; kb < blocks; ++kb) {
+                        const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+                        const bool first = PROMOTE ? kb % seg_blocks == 0 : kb == 0;
+                        if (first) {
+                            if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+                        }
+                        if (!mbar_wait_bounded(&full_a[ca.slot], ca.phase, abort_flag) ||
+                            !mbar_wait_bounded(&full_b[cb.slot], cb.phase, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t a_addr = smem_u32(ring_a + ca.slot * RAG_SLOT);
+                        const uint32_t b_addr = smem_u32(ring_b + cb.slot * RAG_SLOT);
+                        const uint64_t ad = DIR == RAG_NT ? smem_desc_sw128(a_addr) : smem_desc_mn_sw128(a_addr);
+                        const uint64_t bd = DIR == RAG_TN ? smem_desc_mn_sw128(b_addr) : smem_desc_sw128(b_addr);
+                        // one step sums 32 bytes of a K-major row, or 16 rows (2048 bytes) of an MN-major tile
+                        constexpr uint64_t a_step = DIR == RAG_NT ? 2 : 128, b_step = DIR == RAG_TN ? 128 : 2;
+                        constexpr int per_step = I8 ? 32 : 16;
+                        const int left = len - kb * 4 * per_step;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            if (s * per_step >= left) break;
+                            const uint32_t accum = (!first || s != 0) ? 1u : 0u;
+                            if (I8) mma2_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                            else mma2_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                        }
+                        mma2_commit_pair(&empty_a[ca.slot], 0x3);
+                        mma2_commit_pair(&empty_b[cb.slot], 0x3);
+                        issued = true;
+                        ca.next();
+                        cb.next();
+                        if (kb == blocks - 1 || (PROMOTE && kb % seg_blocks == seg_blocks - 1)) {
+                            mma2_commit_pair(&tfull[buf], 0x3);
+                            acc_phase ^= 1u << buf;
+                            buf ^= 1;
+                        }
+                    }
+                    if (!ok) break;
+                }
+                if (*abort_flag && issued) {
+                    mma2_commit_local(drain);
+                    volatile int dummy = 0;
+                    mbar_wait_bounded(drain, 0, &dummy, 100000000ull);
+                }
+            }
+        } else if (warp == 5 && DIR == RAG_TN) {
+            // ---------------------------------------------------- tail rows (both CTAs)
+            RagCursor<SA> ca;
+            RagCursor<SB> cb;
+            uint32_t ph_a = 0, ph_b = 0, ph_p = 0;  // bit s: phase of the slot's landed_a / landed_b / peer_done
+            const uint32_t peer0 = mapa_shared(smem_u32(peer_done), 0);
+            for (int i = cluster_id; i < total; i += n_clusters) {
+                const RagItem it = rag_item<DIR>(P, tab, i);
+                const int blocks = rag_blocks<DIR, I8>(P, it);
+                if ((it.rows & 15) == 0) {
+                    ca.skip(blocks);
+                    cb.skip(blocks);
+                    continue;
+                }
+                ca.skip(blocks - 1);
+                cb.skip(blocks - 1);
+                // every lane waits: each then sees the landed bytes before it overwrites some
+                const bool ok = mbar_wait_bounded(&landed_a[ca.slot], (ph_a >> ca.slot) & 1u, abort_flag) &&
+                                mbar_wait_bounded(&landed_b[cb.slot], (ph_b >> cb.slot) & 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const int r0 = it.rows - (blocks - 1) * 64;  // rows of the group in this block
+                const int n = ((r0 + 15) & ~15) - r0;
+                for (int j = lane; j < n * 32; j += 32) {    // a row is 128 bytes of each 64 x 64 block
+                    const int row = r0 + (j >> 5), blk = (j >> 3) & 3, piece = j & 7;
+                    uint8_t* tile = blk < 2 ? ring_a + ca.slot * RAG_SLOT : ring_b + cb.slot * RAG_SLOT;
+                    *reinterpret_cast<uint4*>(tile + (blk & 1) * RAG_TN_BLOCK + row * 128 + piece * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (!leader) {
+                    if (lane == 0) mbar_arrive_cluster_release(peer0 + (uint32_t)(ca.slot * 8));
+                } else {
+                    int got = 0;
+                    if (lane == 0) got = mbar_wait_bounded_cluster(&peer_done[ca.slot], (ph_p >> ca.slot) & 1u, abort_flag);
+                    if (!__shfl_sync(0xffffffffu, got, 0)) break;
+                    if (lane == 0) {
+                        mbar_arrive(&full_a[ca.slot]);
+                        mbar_arrive(&full_b[cb.slot]);
+                    }
+                }
+                ph_a ^= 1u << ca.slot;
+                ph_b ^= 1u << cb.slot;
+                ph_p ^= 1u << ca.slot;
+                ca.next();
+                cb.next();
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue (both CTAs, own TMEM)
+        if (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RAG_REGS_EPILOGUE));
         const int q = warp & 3;                          // TMEM lane quarter of this warp
         const int half = (warp - RAG_EPI_WARP0) >> 2;
         uint8_t* stage = staging + (warp - RAG_EPI_WARP0) * C::STAGING;
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         uint32_t acc_phase = 0;
         int buf = 0;
+        auto wait_acc = [&]() -> bool {
+            int got = 0;
+            if (lane == 0) got = mbar_wait_bounded(&tfull[buf], (acc_phase >> buf) & 1u, abort_flag) ? 1 : 0;
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if (got) tc_fence_after();
+            return got != 0;
+        };
+        auto release_acc = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * 8));
+            acc_phase ^= 1u << buf;
+            buf ^= 1;
+        };
         for (int i = cluster_id; i < total; i += n_clusters) {
             const RagItem it = rag_item<DIR>(P, tab, i);
             const int f0 = it.m * 256 + (int)rank * 128 + q * 32;
+            const size_t base = (size_t)it.g * P.n * P.k;  // TN: the group's dw
             if (DIR == RAG_TN && it.rows == 0) {
                 if (!P.accumulate && f0 + lane < P.n) {
                     uint8_t* row = static_cast<uint8_t*>(P.y) +
-                                   (((size_t)it.g * P.n + f0 + lane) * P.k + it.col0) * (P.out == MOE_F32 ? 4 : 2);
+                                   (base + (size_t)(f0 + lane) * P.k + it.col0) * (P.out == MOE_F32 ? 4 : 2);
                     const int pieces = it.width * (P.out == MOE_F32 ? 4 : 2) / 16;  // k is a multiple of 8
                     for (int p = half; p < pieces; p += 2) reinterpret_cast<uint4*>(row)[p] = make_uint4(0, 0, 0, 0);
                 }
                 continue;
             }
+            const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+            if (PROMOTE) {
+                // this warp's columns: chunks of 32 at 32 (half + 2 c)
+                const int segs = (rag_blocks<DIR, I8>(P, it) + seg_blocks - 1) / seg_blocks;
+                float sum[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+                bool ok = true;
+                for (int sg = 0; sg < segs; ++sg) {
+                    if (!wait_acc()) { ok = false; break; }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int c0 = 32 * (half + 2 * c);
+                        if (c0 < it.width) {
+                            float v[32];
+                            tmem_ld32(lanes + (uint32_t)(buf * 256 + c0), v);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) add2(sum[c][j], sum[c][j + 1], v[j], v[j + 1]);
+                        }
+                    }
+                    release_acc();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int c0 = 32 * (half + 2 * c);
+                    if (c0 < it.width) {
+                        if (DIR == RAG_TN) rag_store_f32_tile<true>(P, stage, base, f0, it.col0 + c0, sum[c]);
+                        else rag_store_rows_f32(P, stage, it.row0 + c0, it.width - c0, f0, sum[c]);
+                    }
+                }
+                continue;
+            }
             float sw = 0.0f;
             if (I8 && f0 + lane < P.n) sw = __ldg(P.sw + (size_t)it.g * P.n + f0 + lane);
-            int got = 0;
-            if (lane == 0) got = mbar_wait_bounded(&tfull[buf], (acc_phase >> buf) & 1u, abort_flag) ? 1 : 0;
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) break;
-            tc_fence_after();
-            const uint32_t t0 = tmem_base + (uint32_t)(buf * 256) + ((uint32_t)(q * 32) << 16);
+            if (!wait_acc()) break;
+            const uint32_t t0 = lanes + (uint32_t)(buf * 256);
             if (DIR == RAG_TN) {
-                const size_t base = (size_t)it.g * P.n * P.k;
                 for (int c0 = 64 * half; c0 < it.width; c0 += 128) {
                     float v[32];
                     const bool wide = P.out != MOE_F32 && !P.accumulate;
@@ -615,8 +752,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                                                            rag_pack2(v[8 * p + 2], v[8 * p + 3], bf16),
                                                            rag_pack2(v[8 * p + 4], v[8 * p + 5], bf16),
                                                            rag_pack2(v[8 * p + 6], v[8 * p + 7], bf16)));
+                        } else if (P.out == MOE_F32) {
+                            rag_store_f32_tile<true>(P, stage, base, f0, it.col0 + c0 + 32 * h, v);
                         } else {
-                            rag_store_f32_tile(P, stage, base, f0, it.col0 + c0 + 32 * h, v);
+                            rag_store_f32_tile<false>(P, stage, base, f0, it.col0 + c0 + 32 * h, v);
                         }
                     }
                     if (wide) rag_store_h16_tile(P, stage, base, f0, it.col0 + c0);
@@ -635,11 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                     rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, v);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * 8));
-            acc_phase ^= 1u << buf;
-            buf ^= 1;
+            release_acc();
         }
     }
 

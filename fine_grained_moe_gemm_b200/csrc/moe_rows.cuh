@@ -193,7 +193,7 @@ __device__ __forceinline__ int code_of(float x, float s, float inv) {
     return (int)fminf(fmaxf(c, -127.0f), 127.0f);
 }
 
-// sx[r] = max |x[r]| / 127 (1 if that is zero), q = codes.  tx threads (a power of two, a
+// sx[r] = max |x[r]| * (1/127) (1 if that is zero), q = codes.  tx threads (a power of two, a
 // warp at least) share a row, which stays in registers between the two passes: NV pieces
 // of 16 values a thread.
 template <typename T, int NV>
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(512) quantize_int8_kernel(const T* __restrict_
             flip ^= 1;
         }
         if (r >= rows) continue;
-        float s = __fdiv_rn(__uint_as_float(m), 127.0f);
+        float s = __fmul_rn(__uint_as_float(m), 1.0f / 127.0f);
         if (s == 0.0f) s = 1.0f;
         if (t == 0) sx[r] = s;
         // an infinity or a NaN in the row: the scale is not finite and the codes are zero

@@ -387,7 +387,8 @@ MOE_API moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, con
 
 /* 8-bit codes with one scale per row (activations per token; a weight matrix's rows
  * are its output channels, so the same call quantises weights):
- *   sx[r]   = max |x[r, :]| / 127, or 1 where that is zero    fp32 [rows]
+ *   sx[r]   = max |x[r, :]| * c, c the fp32 number nearest to 1/127, rounded once;
+ *             1 where that is zero                            fp32 [rows]
  *   q[r, c] = the integer nearest to the real quotient x[r, c] / sx[r], ties to even,
  *             in [-127, 127]                                  int8 [rows, k]
  * x: [rows, k] MOE_F32, MOE_BF16 or MOE_F16, k a multiple of 16, at most 32768.  A

@@ -178,6 +178,40 @@ def test_wgrad_neighbours_do_not_leak(poison):
     _wgrad_case(RAGGED, 136, 136, BF, FS, seed=12, poison=poison)
 
 
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_long_fp32_sums_keep_their_precision(dtype):
+    """The tensor core cuts its partial sums off; within 512 terms (32 additions) that is at most 32 x 2^-23 of the
+    sum and half of it on average, 2e-6; adding the segments in fp32 must not let it grow with the length."""
+    gen = _gen(21)
+    for m in (512, 513, 4096, 30001):
+        dy, x = _rand(gen, (m, 264), dtype), _rand(gen, (m, 136), dtype)
+        dw = torch.empty((1, 264, 136), device=DEV)
+        moe.moe_grouped_wgrad(dy, x, None, dw)
+        ref = dy.double().t() @ x.double()
+        assert float((dw[0].double() - ref).norm() / ref.norm()) <= 2e-6, m
+    for k in (512, 520, 4096, 18432, 65536):
+        for transpose in (False, True):
+            x, w = _rand(gen, (300, k), dtype), _rand(gen, (1, k, 136) if transpose else (1, 136, k), dtype)
+            y = torch.empty((300, 136), device=DEV)
+            moe.moe_grouped_mm(x, w, None, y, transpose_w=transpose)
+            ref = x.double() @ (w[0].double() if transpose else w[0].double().t())
+            assert float((y.double() - ref).norm() / ref.norm()) <= 2e-6, k
+    assert moe.device_error() == 0
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("strided", [False, True])
+def test_long_fp32_sums_ragged(transpose, strided):
+    _mm_case(RAGGED, 136, 1048, BF, FS, transpose, seed=31, first=2, spare=3, strided=strided, accumulate=True)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_long_fp32_gradients_ragged(accumulate):
+    _wgrad_case([0, 700, 3, 1500, 0, 512, 513, 1025], 136, 264, BF, FS, seed=32, first=1, spare=5, accumulate=accumulate,
+                poison=4)
+    _wgrad_case([700, 3, 1500], 136, 264, FH, FS, seed=33, accumulate=accumulate, poison=1)
+
+
 def test_wgrad_without_rows_is_zero():
     dw = torch.full((3, 16, 24), float("nan"), device=DEV)
     none = torch.empty((0, 16), dtype=BF, device=DEV), torch.empty((0, 24), dtype=BF, device=DEV)
@@ -237,7 +271,8 @@ def test_int8_codes(rows, k, dtype):
     if rows > 4:
         bad[3] = bad[4] = True
         assert bool((q[3:5] == 0).all()) and not bool(sx[3:5].isfinite().any())
-    ref_s = (x.double().abs().amax(1) / 127.0).float()
+    # one fp32 product (the product of two fp32 numbers is exact in 64 bits)
+    ref_s = (x.double().abs().amax(1) * float(np.float32(1) / np.float32(127))).float()
     ref_s = torch.where(ref_s == 0, torch.ones_like(ref_s), ref_s)
     assert torch.equal(sx[~bad], ref_s[~bad])
     ref_q = torch.round(x.double() / ref_s.double()[:, None]).clamp(-127, 127)
@@ -248,7 +283,7 @@ def test_int8_codes_next_to_the_border():
     """fp32 values one ulp around every border of a scale that is no power of two."""
     s = np.float32(0.1234567)
     amax = np.float32(s * np.float32(127.0))
-    s = np.float32(amax / np.float32(127.0))
+    s = np.float32(amax * (np.float32(1) / np.float32(127)))
     mid = ((np.arange(-127, 127) + 0.5) * np.float64(s)).astype(np.float32)
     x = np.concatenate([mid, np.nextafter(mid, np.float32(np.inf)), np.nextafter(mid, np.float32(-np.inf))])
     x = np.concatenate([[amax], x, np.zeros((-len(x) - 1) % 16, np.float32)]).astype(np.float32)
