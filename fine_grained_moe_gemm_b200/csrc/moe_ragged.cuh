@@ -31,7 +31,7 @@
 
 namespace moe {
 
-constexpr int RAG_SLOT = 128 * 128;       // one slot of a ring: 128 features (rows) x 128 bytes of the summed axis
+constexpr int RAG_SLOT = 128 * 128;       // half of a stage: 128 features (rows) x 128 bytes of the summed axis
 constexpr int RAG_TN_BLOCK = 64 * 128;    // one 64 x 64 block of an MN-major tile
 // Warps: 0-3 load (a thread issues one TMA instruction every few hundred cycles whatever
 // its size, and a block of 64 is consumed in about 700), 4 issues the MMAs, 5 zeroes
@@ -56,13 +56,10 @@ template <int DIR>
 struct RagCfg {
     // a staging tile of the epilogue, per warp: 32 rows of 64 (NT, NN) or 128 bytes
     static constexpr int STAGING = DIR == RAG_TN ? 4096 : 2048;
-    // Separate rings: the weights come from HBM and want many bytes under way, the rows
-    // from L2.  TN reads both operands from L2.
-    static constexpr int STAGES_A = DIR == RAG_TN ? 5 : 8;
-    static constexpr int STAGES_B = DIR == RAG_TN ? 5 : 4;
-    static constexpr int RING = (STAGES_A + STAGES_B) * RAG_SLOT;
+    static constexpr int STAGES = DIR == RAG_TN ? 5 : 6;
+    static constexpr int RING = STAGES * 2 * RAG_SLOT;
     static constexpr int TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;  // first row, rows, first item of each group
-    static constexpr int BARS = 2 * (STAGES_A + STAGES_B) + (DIR == RAG_TN ? 2 * STAGES_A + STAGES_B : 0) + 5;
+    static constexpr int BARS = 2 * STAGES + (DIR == RAG_TN ? 2 * STAGES : 0) + 5;
     static constexpr int MISC = (BARS * 8 + (2 + RAG_THREADS / 32) * 4 + 15) / 16 * 16;
     static constexpr int SMEM_BYTES = 1024 + RING + RAG_EPI_WARPS * STAGING + TABLE + MISC;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -440,27 +437,23 @@ template <int DIR, bool I8, bool PROMOTE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
     moe_ragged_kernel(const __grid_constant__ RaggedArgs P) {
     using C = RagCfg<DIR>;
-    constexpr int SA = C::STAGES_A, SB = C::STAGES_B;
+    constexpr int ST = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* ring_a = smem;
-    uint8_t* ring_b = smem + SA * RAG_SLOT;
+    uint8_t* ring = smem;
     uint8_t* staging = smem + C::RING;
     RagTable tab;
     tab.start = reinterpret_cast<int*>(staging + RAG_EPI_WARPS * C::STAGING);
     tab.count = tab.start + RAG_MAX_GROUPS;
     tab.first = tab.count + RAG_MAX_GROUPS;
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tab.start) + C::TABLE);
-    uint64_t* full_a = bars;               // leader: both CTAs' bytes of the slot are there
-    uint64_t* full_b = full_a + SA;
-    uint64_t* empty_a = full_b + SB;       // both: slot consumed
-    uint64_t* empty_b = empty_a + SA;
-    uint64_t* tfull = empty_b + SB;        // [2] both: accumulator written
+    uint64_t* full = bars;                 // leader: both CTAs' bytes of the stage are there
+    uint64_t* empty = full + ST;           // both: stage consumed
+    uint64_t* tfull = empty + ST;          // [2] both: accumulator written
     uint64_t* tempty = tfull + 2;          // [2] leader: accumulator read by both epilogues
     uint64_t* drain = tempty + 2;
-    uint64_t* landed_a = drain + 1;        // TN, blocks with tail rows, both: this CTA's bytes
-    uint64_t* landed_b = landed_a + SA;
-    uint64_t* peer_done = landed_b + SB;   // TN, blocks with tail rows, leader: the peer's tail is zeroed
+    uint64_t* landed = drain + 1;          // TN, blocks with tail rows, both: this CTA's bytes
+    uint64_t* peer_done = landed + ST;     // TN, blocks with tail rows, leader: the peer's tail is zeroed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* warp_sums = reinterpret_cast<int*>(tmem_slot + 2);  // [RAG_THREADS / 32]
@@ -502,15 +495,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                 const uint64_t pol_stream = l2_policy_evict_first();
                 const uint64_t pol_keep = l2_policy_evict_last();
                 const uint64_t pol_normal = l2_policy_evict_normal();
-                uint64_t* full = is_a ? full_a : full_b;
-                uint64_t* empty = is_a ? empty_a : empty_b;
-                uint64_t* landed = is_a ? landed_a : landed_b;
-                uint8_t* ring = is_a ? ring_a : ring_b;
-                const int n_slots = is_a ? SA : SB;
                 const uint32_t full0 = mapa_shared(smem_u32(full), 0);
                 const uint32_t landed0 = mapa_shared(smem_u32(landed), rank);
-                int slot = 0;
-                uint32_t phase = 0;
+                RagCursor<ST> at;
                 for (int i = cluster_id; i < total; i += n_clusters) {
                     const RagItem it = rag_item<DIR>(P, tab, i);
                     const int blocks = rag_blocks<DIR, I8>(P, it);
@@ -522,20 +509,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                     const int box = nh > 64 ? 128 : nh > 16 ? 64 : 16;
                     const CUtensorMap* bmap = nh > 64 ? &P.b128 : nh > 16 ? &P.b64 : &P.b16;
                     const bool second = nh > 64;                 // TN: B has a second 64-column block
-                    const uint32_t bytes = is_a ? (uint32_t)RAG_SLOT
-                                           : DIR == RAG_TN ? (second ? 2u : 1u) * RAG_TN_BLOCK : (uint32_t)box * 128u;
+                    const uint32_t bytes =
+                        RAG_SLOT + (DIR == RAG_TN ? (second ? 2u : 1u) * RAG_TN_BLOCK : (uint32_t)box * 128u);
                     const int brow = it.row0 + (int)rank * nh;
                     bool ok = true;
                     for (int kb = 0; kb < blocks; ++kb) {
-                        if (!mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag)) { ok = false; break; }
-                        uint8_t* dst = ring + slot * RAG_SLOT + half * 128;
+                        if (!mbar_wait_bounded(&empty[at.slot], at.phase ^ 1u, abort_flag)) { ok = false; break; }
+                        uint8_t* dst = ring + at.slot * 2 * RAG_SLOT + (is_a ? 0 : RAG_SLOT) + half * 128;
                         // a block whose last rows belong to the next group is counted where it lies,
                         // for the warp that zeroes them; the others on the leader's barrier
                         const bool tail = DIR == RAG_TN && kb == blocks - 1 && (it.rows & 15);
-                        const uint32_t bar = (tail ? landed0 : full0) + (uint32_t)(slot * 8);
-                        if (half == 0) {
-                            if (tail) mbar_arrive_expect_tx(&landed[slot], bytes);
-                            else if (leader) mbar_arrive_expect_tx(&full[slot], 2u * bytes);
+                        const uint32_t bar = (tail ? landed0 : full0) + (uint32_t)(at.slot * 8);
+                        if (warp == 0) {
+                            if (tail) mbar_arrive_expect_tx(&landed[at.slot], bytes);
+                            else if (leader) mbar_arrive_expect_tx(&full[at.slot], 2u * bytes);
                         }
                         if (DIR == RAG_TN) {
                             if (is_a) tma_load_2d_pair(dst, &P.a, f0 + half, it.row0 + kb * 64, bar, policy);
@@ -549,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                         } else {
                             tma_load_3d_pair(dst, &P.a, f0 + half, kb * 64, it.g, bar, policy);
                         }
-                        if (++slot == n_slots) { slot = 0; phase ^= 1u; }
+                        at.next();
                     }
                     if (!ok) break;
                 }
@@ -557,55 +544,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
         } else if (warp == 4) {
             if (lane == 0 && leader) {
                 // ------------------------------------------------ 2-SM MMA issuer
-                RagCursor<SA> ca;
-                RagCursor<SB> cb;
+                RagCursor<ST> at;
                 uint32_t acc_phase = 0;  // bit b: phase of accumulator b
                 int buf = 0;
                 bool issued = false;
-                for (int i = cluster_id; i < total; i += n_clusters) {
+                // one step sums 32 bytes of a K-major row, or 16 rows (2048 bytes) of an MN-major tile
+                constexpr uint64_t a_step = DIR == RAG_NT ? 2 : 128, b_step = DIR == RAG_TN ? 128 : 2;
+                constexpr int per_step = I8 ? 32 : 16;
+                constexpr uint64_t stage_step = 2 * RAG_SLOT / 16;
+                const uint32_t ring_addr = smem_u32(ring);
+                const uint64_t ad0 = DIR == RAG_NT ? smem_desc_sw128(ring_addr) : smem_desc_mn_sw128(ring_addr);
+                const uint64_t bd0 = DIR == RAG_TN ? smem_desc_mn_sw128(ring_addr + RAG_SLOT)
+                                                   : smem_desc_sw128(ring_addr + RAG_SLOT);
+                bool ok = true;
+                for (int i = cluster_id; ok && i < total; i += n_clusters) {
                     const RagItem it = rag_item<DIR>(P, tab, i);
                     const int blocks = rag_blocks<DIR, I8>(P, it);
-                    // elements of the summed axis: the last block ends with it (TN: rows past it are
-                    // zero up to a multiple of 16; NT, NN: the loads filled in zeros)
-                    const int len = DIR == RAG_TN ? it.rows : P.k;
+                    // elements of the summed axis in the last block (TN: rows past it are zero up to a
+                    // multiple of 16; NT, NN: the loads filled in zeros)
+                    const int last = (DIR == RAG_TN ? it.rows : P.k) - (blocks - 1) * 4 * per_step;
                     const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, (uint32_t)rag_mma_n<DIR>(it));
-                    bool ok = true;
-                    for (int kb = 0; kb < blocks; ++kb) {
+                    for (int kb0 = 0; kb0 < blocks; kb0 += PROMOTE ? seg_blocks : blocks) {
+                        const int kb1 = PROMOTE ? min(kb0 + seg_blocks, blocks) : blocks;
+                        if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
                         const uint32_t d = tmem_base + (uint32_t)(buf * 256);
-                        const bool first = PROMOTE ? kb % seg_blocks == 0 : kb == 0;
-                        if (first) {
-                            if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-                        }
-                        if (!mbar_wait_bounded(&full_a[ca.slot], ca.phase, abort_flag) ||
-                            !mbar_wait_bounded(&full_b[cb.slot], cb.phase, abort_flag)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t a_addr = smem_u32(ring_a + ca.slot * RAG_SLOT);
-                        const uint32_t b_addr = smem_u32(ring_b + cb.slot * RAG_SLOT);
-                        const uint64_t ad = DIR == RAG_NT ? smem_desc_sw128(a_addr) : smem_desc_mn_sw128(a_addr);
-                        const uint64_t bd = DIR == RAG_TN ? smem_desc_mn_sw128(b_addr) : smem_desc_sw128(b_addr);
-                        // one step sums 32 bytes of a K-major row, or 16 rows (2048 bytes) of an MN-major tile
-                        constexpr uint64_t a_step = DIR == RAG_NT ? 2 : 128, b_step = DIR == RAG_TN ? 128 : 2;
-                        constexpr int per_step = I8 ? 32 : 16;
-                        const int left = len - kb * 4 * per_step;
+                        for (int kb = kb0; kb < kb1; ++kb) {
+                            if (!mbar_wait_bounded(&full[at.slot], at.phase, abort_flag)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint64_t ad = ad0 + stage_step * at.slot, bd = bd0 + stage_step * at.slot;
+                            const int steps = kb == blocks - 1 ? (last + per_step - 1) / per_step : 4;
+                            if (steps == 4) {
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            if (s * per_step >= left) break;
-                            const uint32_t accum = (!first || s != 0) ? 1u : 0u;
-                            if (I8) mma2_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
-                            else mma2_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                                for (int s = 0; s < 4; ++s) {
+                                    const uint32_t accum = (kb > kb0 || s != 0) ? 1u : 0u;
+                                    if (I8) mma2_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                                    else mma2_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                                }
+                            } else {
+                                for (int s = 0; s < steps; ++s) {
+                                    const uint32_t accum = (kb > kb0 || s != 0) ? 1u : 0u;
+                                    if (I8) mma2_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                                    else mma2_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                                }
+                            }
+                            mma2_commit_pair(&empty[at.slot], 0x3);
+                            issued = true;
+                            at.next();
                         }
-                        mma2_commit_pair(&empty_a[ca.slot], 0x3);
-                        mma2_commit_pair(&empty_b[cb.slot], 0x3);
-                        issued = true;
-                        ca.next();
-                        cb.next();
-                        if (kb == blocks - 1 || (PROMOTE && kb % seg_blocks == seg_blocks - 1)) {
-                            mma2_commit_pair(&tfull[buf], 0x3);
-                            acc_phase ^= 1u << buf;
-                            buf ^= 1;
-                        }
+                        if (!ok) break;
+                        mma2_commit_pair(&tfull[buf], 0x3);
+                        acc_phase ^= 1u << buf;
+                        buf ^= 1;
                     }
-                    if (!ok) break;
                 }
                 if (*abort_flag && issued) {
                     mma2_commit_local(drain);
@@ -615,50 +605,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
             }
         } else if (warp == 5 && DIR == RAG_TN) {
             // ---------------------------------------------------- tail rows (both CTAs)
-            RagCursor<SA> ca;
-            RagCursor<SB> cb;
-            uint32_t ph_a = 0, ph_b = 0, ph_p = 0;  // bit s: phase of the slot's landed_a / landed_b / peer_done
+            RagCursor<ST> at;
+            uint32_t ph = 0;  // bit s: phase of the stage's landed and peer_done
             const uint32_t peer0 = mapa_shared(smem_u32(peer_done), 0);
             for (int i = cluster_id; i < total; i += n_clusters) {
                 const RagItem it = rag_item<DIR>(P, tab, i);
                 const int blocks = rag_blocks<DIR, I8>(P, it);
                 if ((it.rows & 15) == 0) {
-                    ca.skip(blocks);
-                    cb.skip(blocks);
+                    at.skip(blocks);
                     continue;
                 }
-                ca.skip(blocks - 1);
-                cb.skip(blocks - 1);
+                at.skip(blocks - 1);
                 // every lane waits: each then sees the landed bytes before it overwrites some
-                const bool ok = mbar_wait_bounded(&landed_a[ca.slot], (ph_a >> ca.slot) & 1u, abort_flag) &&
-                                mbar_wait_bounded(&landed_b[cb.slot], (ph_b >> cb.slot) & 1u, abort_flag);
+                const bool ok = mbar_wait_bounded(&landed[at.slot], (ph >> at.slot) & 1u, abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const int r0 = it.rows - (blocks - 1) * 64;  // rows of the group in this block
                 const int n = ((r0 + 15) & ~15) - r0;
                 for (int j = lane; j < n * 32; j += 32) {    // a row is 128 bytes of each 64 x 64 block
                     const int row = r0 + (j >> 5), blk = (j >> 3) & 3, piece = j & 7;
-                    uint8_t* tile = blk < 2 ? ring_a + ca.slot * RAG_SLOT : ring_b + cb.slot * RAG_SLOT;
-                    *reinterpret_cast<uint4*>(tile + (blk & 1) * RAG_TN_BLOCK + row * 128 + piece * 16) =
+                    *reinterpret_cast<uint4*>(ring + at.slot * 2 * RAG_SLOT + blk * RAG_TN_BLOCK + row * 128 + piece * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (!leader) {
-                    if (lane == 0) mbar_arrive_cluster_release(peer0 + (uint32_t)(ca.slot * 8));
+                    if (lane == 0) mbar_arrive_cluster_release(peer0 + (uint32_t)(at.slot * 8));
                 } else {
                     int got = 0;
-                    if (lane == 0) got = mbar_wait_bounded_cluster(&peer_done[ca.slot], (ph_p >> ca.slot) & 1u, abort_flag);
+                    if (lane == 0) got = mbar_wait_bounded_cluster(&peer_done[at.slot], (ph >> at.slot) & 1u, abort_flag);
                     if (!__shfl_sync(0xffffffffu, got, 0)) break;
-                    if (lane == 0) {
-                        mbar_arrive(&full_a[ca.slot]);
-                        mbar_arrive(&full_b[cb.slot]);
-                    }
+                    if (lane == 0) mbar_arrive(&full[at.slot]);
                 }
-                ph_a ^= 1u << ca.slot;
-                ph_b ^= 1u << cb.slot;
-                ph_p ^= 1u << ca.slot;
-                ca.next();
-                cb.next();
+                ph ^= 1u << at.slot;
+                at.next();
             }
         }
     } else {
