@@ -652,37 +652,84 @@ def moe_quantize_act(x, q, sx, stream=None):
 
 
 # ---------------------------------------------------------------- products by group
+# A decode step's calls run for a few microseconds each, so these wrappers pass plain
+# integers and look each property of a tensor up once (about 6 us a call; 15 with the
+# helpers above).
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 _HALVES = (torch.bfloat16, torch.float16)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_I8 = (torch.int8,)
+_call_cache = {}
 
 
-def _rows(t, name: str, shape, dtypes) -> int:
-    """Checks a 2-D CUDA tensor whose rows may lie apart (a slice of a wider buffer); returns their distance."""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
-    if t.device.index != torch.cuda.current_device():
+def _entry(name: str):
+    """A C entry point of the library (``lib()`` takes a lock and finds the function by name on every call)."""
+    L = _lib
+    if L is None or _call_cache.get("lib") is not L:
+        L = lib()
+        _call_cache.clear()
+        _call_cache["lib"] = L
+    f = _call_cache.get(name)
+    if f is None:
+        f = _call_cache[name] = getattr(L, name)
+    return f
+
+
+def _stream_int(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _home(t, name: str) -> int:
+    """The current device, which must be the tensor's."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if d != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    _shape(t, name, shape, dtypes)
-    if t.shape[0] <= 1:  # one row or none: torch leaves the stride open
-        step = 16 // t.element_size()
-        return (t.shape[1] + step - 1) // step * step
-    return t.stride(0)
+    return d
 
 
-def _offsets(offsets, groups: int):
+def _dense(t, name: str, device: int, shape, dtypes) -> int:
+    """Address of a contiguous tensor on `device` of the given shape and one of the types."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{device}")
+    if t.shape != shape or t.dtype not in dtypes:
+        _shape(t, name, shape, dtypes)
+    return t.data_ptr()
+
+
+def _rows(t, name: str, device: int, shape, dtypes):
+    """Address and distance of the rows of a matrix on `device` whose rows may lie apart (a slice of a wider buffer)."""
+    if t.get_device() != device or t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix on cuda:{device}")
+    if t.shape != shape or t.dtype not in dtypes:
+        _shape(t, name, shape, dtypes)
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if shape[0] <= 1:  # one row or none: torch leaves the stride open
+        e = 16 // t.element_size()
+        ld = (shape[1] + e - 1) // e * e
+    return t.data_ptr(), ld
+
+
+def _offsets(offsets, groups: int, device: int):
     if offsets is None:
         if groups != 1:
             raise ValueError("offsets: only one group can go without")
-        return
-    _dev(offsets, "offsets")
-    _shape(offsets, "offsets", (groups + 1,), (torch.int32,))
+        return None
+    return _dense(offsets, "offsets", device, (groups + 1,), _I32)
 
 
-def _count(n_rows):
-    if n_rows is not None:
-        _dev(n_rows, "n_rows")
-        if n_rows.dtype != torch.int32 or n_rows.numel() != 1:
-            raise ValueError("n_rows: one int32 on the device")
+def _optional(t, name: str, device: int, shape, dtypes):
+    return None if t is None else _dense(t, name, device, shape, dtypes)
+
+
+def _count(n_rows, device: int):
+    return None if n_rows is None else _dense(n_rows.view(-1), "n_rows", device, (1,), _I32)
 
 
 def moe_grouped_mm(x, w, offsets, y, transpose_w: bool = False, accumulate: bool = False, stream=None):
@@ -690,100 +737,95 @@ def moe_grouped_mm(x, w, offsets, y, transpose_w: bool = False, accumulate: bool
     x [R, k], w [G, n, k] (``transpose_w``: [G, k, n], the product with w itself, which is the input gradient of the
     other form), bf16 or f16; y [R, n] of that type or fp32.  Rows of x and y may be slices of wider buffers; rows
     outside the groups are left as they were."""
-    _dev(w, "w")
-    if w.dim() != 3 or w.dtype not in _HALVES:
-        raise ValueError(f"w: {tuple(w.shape)} {w.dtype}, expected three dimensions, bf16 or f16")
-    G, n, k = w.shape
+    dev, wt = _home(w, "w"), w.dtype
+    if w.dim() != 3 or wt not in _HALVES:
+        raise ValueError(f"w: {tuple(w.shape)} {wt}, expected three dimensions, bf16 or f16")
+    shape = w.shape
+    G, n, k = shape
+    pw = _dense(w, "w", dev, shape, _HALVES)
     if transpose_w:
         n, k = k, n
     R = x.shape[0]
-    ldx = _rows(x, "x", (R, k), (w.dtype,))
-    ldy = _rows(y, "y", (R, n), (w.dtype, torch.float32))
-    _offsets(offsets, G)
-    _check(lib().moe_grouped_mm(G, R, n, k, _FLOATS[w.dtype], _p(x), ldx, _p(w), 1 if transpose_w else 0, _p(offsets),
-                                _p(y), ldy, _FLOATS[y.dtype], 1 if accumulate else 0, _stream(stream)),
-           "moe_grouped_mm")
+    px, ldx = _rows(x, "x", dev, (R, k), (wt,))
+    py, ldy = _rows(y, "y", dev, (R, n), (wt, torch.float32))
+    _check(_entry("moe_grouped_mm")(G, R, n, k, _FLOATS[wt], px, ldx, pw, 1 if transpose_w else 0,
+                                    _offsets(offsets, G, dev), py, ldy, _FLOATS[y.dtype], 1 if accumulate else 0,
+                                    _stream_int(stream, dev)), "moe_grouped_mm")
 
 
 def moe_grouped_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=None):
     """dw[g] (+)= dy[rows of g]^T . x[rows of g]: the weight gradient of ``moe_grouped_mm``.  dy [R, n] and x [R, k]
     bf16 or f16; dw [G, n, k] of that type or fp32; an empty group's gradient is zero."""
-    _dev(dw, "dw")
+    dev, xt = _home(dw, "dw"), x.dtype
     if dw.dim() != 3:
         raise ValueError(f"dw: {tuple(dw.shape)}, expected three dimensions")
-    G, n, k = dw.shape
+    shape = dw.shape
+    G, n, k = shape
     R = x.shape[0]
-    ldx = _rows(x, "x", (R, k), _HALVES)
-    lddy = _rows(dy, "dy", (R, n), (x.dtype,))
-    _shape(dw, "dw", (G, n, k), (x.dtype, torch.float32))
-    _offsets(offsets, G)
-    _check(lib().moe_grouped_wgrad(G, R, n, k, _FLOATS[x.dtype], _p(dy), lddy, _p(x), ldx, _p(offsets), _p(dw),
-                                   _FLOATS[dw.dtype], 1 if accumulate else 0, _stream(stream)), "moe_grouped_wgrad")
-
-
-def _coef(t, name: str, R: int):
-    if t is not None:
-        _dev(t, name)
-        _shape(t, name, (R,), (torch.float32,))
+    px, ldx = _rows(x, "x", dev, (R, k), _HALVES)
+    pdy, lddy = _rows(dy, "dy", dev, (R, n), (xt,))
+    pdw = _dense(dw, "dw", dev, shape, (xt, torch.float32))
+    _check(_entry("moe_grouped_wgrad")(G, R, n, k, _FLOATS[xt], pdy, lddy, px, ldx, _offsets(offsets, G, dev), pdw,
+                                       _FLOATS[dw.dtype], 1 if accumulate else 0, _stream_int(stream, dev)),
+           "moe_grouped_wgrad")
 
 
 def moe_swiglu(gate, up, h, coef=None, n_rows=None, stream=None):
     """h = coef * SiLU(gate) * up per row ([R, width], fp32, bf16 or f16; coef fp32 [R] or None).  ``n_rows``: one
     int32 on the device, the rows to compute (e.g. ``offsets[-1:]``); the rows behind are left as they were.  h may
     be gate or up."""
-    shape, t = tuple(gate.shape), (gate.dtype,)
-    ldg = _rows(gate, "gate", shape, tuple(_FLOATS))
-    ldu, ldh = _rows(up, "up", shape, t), _rows(h, "h", shape, t)
-    _coef(coef, "coef", shape[0])
-    _count(n_rows)
-    _check(lib().moe_swiglu(shape[0], shape[1], _FLOATS[gate.dtype], _p(gate), ldg, _p(up), ldu, _p(coef), _p(n_rows),
-                            _p(h), ldh, _stream(stream)), "moe_swiglu")
+    dev, shape, t = _home(gate, "gate"), gate.shape, (gate.dtype,)
+    pg, ldg = _rows(gate, "gate", dev, shape, _FLOATS)
+    pu, ldu = _rows(up, "up", dev, shape, t)
+    ph, ldh = _rows(h, "h", dev, shape, t)
+    R, width = shape
+    _check(_entry("moe_swiglu")(R, width, _FLOATS[gate.dtype], pg, ldg, pu, ldu, _optional(coef, "coef", dev, (R,), _F32),
+                                _count(n_rows, dev), ph, ldh, _stream_int(stream, dev)), "moe_swiglu")
 
 
 def moe_swiglu_backward(dh, gate, up, dgate, dup, coef=None, dcoef=None, n_rows=None, stream=None):
     """The gradients of ``moe_swiglu``: dgate, dup (like gate), and dcoef fp32 [R] when given.  dgate may be gate,
     dup may be up or dh."""
-    shape, t = tuple(gate.shape), (gate.dtype,)
-    ldg = _rows(gate, "gate", shape, tuple(_FLOATS))
-    lds = [_rows(v, name, shape, t) for name, v in (("dh", dh), ("up", up), ("dgate", dgate), ("dup", dup))]
-    _coef(coef, "coef", shape[0])
-    _coef(dcoef, "dcoef", shape[0])
-    _count(n_rows)
-    _check(lib().moe_swiglu_backward(shape[0], shape[1], _FLOATS[gate.dtype], _p(dh), lds[0], _p(gate), ldg, _p(up),
-                                     lds[1], _p(coef), _p(n_rows), _p(dgate), lds[2], _p(dup), lds[3], _p(dcoef),
-                                     _stream(stream)), "moe_swiglu_backward")
+    dev, shape, t = _home(gate, "gate"), gate.shape, (gate.dtype,)
+    pg, ldg = _rows(gate, "gate", dev, shape, _FLOATS)
+    pd, ldd = _rows(dh, "dh", dev, shape, t)
+    pu, ldu = _rows(up, "up", dev, shape, t)
+    pdg, lddg = _rows(dgate, "dgate", dev, shape, t)
+    pdu, lddu = _rows(dup, "dup", dev, shape, t)
+    R, width = shape
+    _check(_entry("moe_swiglu_backward")(R, width, _FLOATS[gate.dtype], pd, ldd, pg, ldg, pu, ldu,
+                                         _optional(coef, "coef", dev, (R,), _F32), _count(n_rows, dev), pdg, lddg, pdu,
+                                         lddu, _optional(dcoef, "dcoef", dev, (R,), _F32), _stream_int(stream, dev)),
+           "moe_swiglu_backward")
 
 
 def moe_quantize_int8(x, q, sx, n_rows=None, stream=None):
     """int8 codes q [R, k] and fp32 scales sx [R] of the rows of x [R, k] (fp32, bf16 or f16): sx = max|x| * fp32(1/127),
     q the nearest integer of x / sx, ties to even.  Weights [.., n, k] quantise per output channel through a view of
     their rows."""
+    dev = _home(x, "x")
+    px, ldx = _rows(x, "x", dev, x.shape, _FLOATS)
     R, k = x.shape
-    ldx = _rows(x, "x", (R, k), tuple(_FLOATS))
-    for name, t, shape, dt in (("q", q, (R, k), torch.int8), ("sx", sx, (R,), torch.float32)):
-        _dev(t, name)
-        _shape(t, name, shape, (dt,))
-    _count(n_rows)
-    _check(lib().moe_quantize_int8(_p(x), _FLOATS[x.dtype], ldx, R, k, _p(n_rows), _p(q), _p(sx), _stream(stream)),
-           "moe_quantize_int8")
+    _check(_entry("moe_quantize_int8")(px, _FLOATS[x.dtype], ldx, R, k, _count(n_rows, dev),
+                                       _dense(q, "q", dev, (R, k), _I8), _dense(sx, "sx", dev, (R,), _F32),
+                                       _stream_int(stream, dev)), "moe_quantize_int8")
 
 
 def moe_grouped_mm_int8(q, sx, w, sw, offsets, y, accumulate: bool = False, stream=None):
     """y[r] (+)= sx[r] sw[g] (q[r] . w[g]^T) with exact integer sums: q [R, k], w [G, n, k] int8, sx [R], sw [G, n]
     fp32, y [R, n] fp32, bf16 or f16; offsets as in ``moe_grouped_mm``."""
-    for name, t in (("q", q), ("sx", sx), ("w", w), ("sw", sw)):
-        _dev(t, name)
+    dev = _home(w, "w")
     if w.dim() != 3:
         raise ValueError(f"w: {tuple(w.shape)}, expected three dimensions")
-    G, n, k = w.shape
+    shape = w.shape
+    G, n, k = shape
     R = q.shape[0]
-    for name, t, shape, dt in (("q", q, (R, k), torch.int8), ("sx", sx, (R,), torch.float32), ("w", w, (G, n, k), torch.int8),
-                               ("sw", sw, (G, n), torch.float32)):
-        _shape(t, name, shape, (dt,))
-    ldy = _rows(y, "y", (R, n), tuple(_FLOATS))
-    _offsets(offsets, G)
-    _check(lib().moe_grouped_mm_int8(G, R, n, k, _p(q), _p(sx), _p(w), _p(sw), _p(offsets), _p(y), ldy,
-                                     _FLOATS[y.dtype], 1 if accumulate else 0, _stream(stream)), "moe_grouped_mm_int8")
+    pq, psx = _dense(q, "q", dev, (R, k), _I8), _dense(sx, "sx", dev, (R,), _F32)
+    pw, psw = _dense(w, "w", dev, shape, _I8), _dense(sw, "sw", dev, (G, n), _F32)
+    py, ldy = _rows(y, "y", dev, (R, n), _FLOATS)
+    _check(_entry("moe_grouped_mm_int8")(G, R, n, k, pq, psx, pw, psw, _offsets(offsets, G, dev), py, ldy,
+                                         _FLOATS[y.dtype], 1 if accumulate else 0, _stream_int(stream, dev)),
+           "moe_grouped_mm_int8")
 
 
 def device_error(stream=None) -> int:

@@ -1421,8 +1421,10 @@ template <typename T>
 static void launch_swiglu_t(bool backward, const SwigluArgs& a, int n_sm, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     const int vecs = a.width / V;
+    // A warp takes a row (its sum needs no barrier) where rows fill the GPU; few rows are
+    // spread over up to a CTA's threads each.
     int tx = 8;
-    while (tx < vecs && tx < ROWS_THREADS) tx *= 2;
+    while (tx < vecs && tx < ROWS_THREADS && (tx < 32 || (long long)a.rows * tx < (long long)n_sm * 2048)) tx *= 2;
     const int rows_per_cta = ROWS_THREADS / tx;
     const int want = (a.rows + rows_per_cta - 1) / rows_per_cta;
     const int grid = want < n_sm * 8 ? want : n_sm * 8;

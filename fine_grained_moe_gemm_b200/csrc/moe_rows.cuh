@@ -82,8 +82,12 @@ __device__ __forceinline__ float row_sigmoid(float z) {
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
 
-// h = c * silu(gate) * up.  tx threads (a power of two) share a row, 256 / tx rows a CTA.
-// h may be gate or up: a thread writes only the piece it has read.
+// How the row operators share out rows: tx threads (a power of two) take a row together,
+// ROWS_THREADS / tx rows a CTA, and a thread works on ROWS_BATCH 16-byte pieces at a time
+// so that their loads are under way together.
+constexpr int ROWS_BATCH = 2;
+
+// h = c * silu(gate) * up.  h may be gate or up: a thread writes only pieces it has read.
 template <typename T>
 __global__ void __launch_bounds__(ROWS_THREADS) swiglu_kernel(const __grid_constant__ SwigluArgs A, int tx) {
     constexpr int V = Vec16<T>::N;
@@ -95,13 +99,25 @@ __global__ void __launch_bounds__(ROWS_THREADS) swiglu_kernel(const __grid_const
         const T* u = static_cast<const T*>(A.up) + (size_t)r * A.ld_up;
         T* h = static_cast<T*>(A.out0) + (size_t)r * A.ld_out0;
         const float c = A.coef ? A.coef[r] : 1.0f;
-        for (int i = t * V; i < A.width; i += tx * V) {
-            Vec16<T> a, b;
-            vec_load(g + i, a);
-            vec_load(u + i, b);
+        for (int i0 = t * V; i0 < A.width; i0 += ROWS_BATCH * tx * V) {
+            Vec16<T> a[ROWS_BATCH], b[ROWS_BATCH];
 #pragma unroll
-            for (int j = 0; j < V; ++j) a.v[j] = c * (a.v[j] * row_sigmoid<T>(a.v[j]) * b.v[j]);
-            vec_store(h + i, a);
+            for (int k = 0; k < ROWS_BATCH; ++k) {
+                const int i = i0 + k * tx * V;
+                if (i < A.width) {
+                    vec_load(g + i, a[k]);
+                    vec_load(u + i, b[k]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < ROWS_BATCH; ++k) {
+                const int i = i0 + k * tx * V;
+                if (i < A.width) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) a[k].v[j] = c * (a[k].v[j] * row_sigmoid<T>(a[k].v[j]) * b[k].v[j]);
+                    vec_store(h + i, a[k]);
+                }
+            }
         }
     }
 }
@@ -116,7 +132,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) swiglu_backward_kernel(const __g
     const int ty = ROWS_THREADS / tx;
     const int rows = rows_to_compute(A.n_rows, A.rows);
     int flip = 0;
-    // every thread of the CTA makes the same number of turns (the reduction synchronises)
+    // every thread of the CTA makes the same number of turns (the reduction may synchronise)
     for (int r0 = blockIdx.x * ty; r0 < rows; r0 += gridDim.x * ty) {
         const int r = r0 + threadIdx.x / tx;
         float dot = 0.0f;
@@ -127,22 +143,34 @@ __global__ void __launch_bounds__(ROWS_THREADS) swiglu_backward_kernel(const __g
             T* dg = static_cast<T*>(A.out0) + (size_t)r * A.ld_out0;
             T* du = static_cast<T*>(A.out1) + (size_t)r * A.ld_out1;
             const float c = A.coef ? A.coef[r] : 1.0f;
-            for (int i = t * V; i < A.width; i += tx * V) {
-                Vec16<T> a, b, e;
-                vec_load(g + i, a);
-                vec_load(u + i, b);
-                vec_load(d + i, e);
+            for (int i0 = t * V; i0 < A.width; i0 += ROWS_BATCH * tx * V) {
+                Vec16<T> a[ROWS_BATCH], b[ROWS_BATCH], e[ROWS_BATCH];
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float s = row_sigmoid<T>(a.v[j]);
-                    const float act = a.v[j] * s;
-                    const float ce = c * e.v[j];
-                    dot = fmaf(e.v[j] * act, b.v[j], dot);
-                    a.v[j] = ce * b.v[j] * fmaf(act, 1.0f - s, s);
-                    b.v[j] = ce * act;
+                for (int k = 0; k < ROWS_BATCH; ++k) {
+                    const int i = i0 + k * tx * V;
+                    if (i < A.width) {
+                        vec_load(g + i, a[k]);
+                        vec_load(u + i, b[k]);
+                        vec_load(d + i, e[k]);
+                    }
                 }
-                vec_store(dg + i, a);
-                vec_store(du + i, b);
+#pragma unroll
+                for (int k = 0; k < ROWS_BATCH; ++k) {
+                    const int i = i0 + k * tx * V;
+                    if (i < A.width) {
+#pragma unroll
+                        for (int j = 0; j < V; ++j) {
+                            const float s = row_sigmoid<T>(a[k].v[j]);
+                            const float act = a[k].v[j] * s;
+                            const float ce = c * e[k].v[j];
+                            dot = fmaf(e[k].v[j] * act, b[k].v[j], dot);
+                            a[k].v[j] = ce * b[k].v[j] * fmaf(act, 1.0f - s, s);
+                            b[k].v[j] = ce * act;
+                        }
+                        vec_store(dg + i, a[k]);
+                        vec_store(du + i, b[k]);
+                    }
+                }
             }
         }
         if (A.dcoef) {  // fixed order: lanes by a butterfly, then the row's warps one after another
@@ -161,30 +189,62 @@ __global__ void __launch_bounds__(ROWS_THREADS) swiglu_backward_kernel(const __g
 }
 
 // ---------------------------------------------------------------- int8 codes
-// Largest magnitude by its bits: non-negative floats order as integers, and a NaN's bits
-// lie above infinity's, so it wins.
-__device__ __forceinline__ uint32_t abs_bits_max(uint32_t m, const float (&v)[16]) {
+// Sixteen values as they lie in memory, and pairs of them in fp32.
+template <typename T>
+struct Raw16 {
+    uint4 u[sizeof(T)];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int i = 0; i < (int)sizeof(T); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ uint32_t word(int i) const {
+        const uint4& v = u[i >> 2];
+        return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    }
+    // values 2 i and 2 i + 1
+    __device__ __forceinline__ float2 pair(int i) const;
+    // Largest magnitude by its bits: non-negative floats order as integers, and a NaN's
+    // bits lie above infinity's, so it wins.  `m` starts at 0; 16-bit types keep a maximum
+    // for each half of a word.
+    __device__ __forceinline__ uint32_t magnitude(uint32_t m) const;
+};
+template <> __device__ __forceinline__ float2 Raw16<float>::pair(int i) const {
+    return make_float2(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+}
+template <> __device__ __forceinline__ float2 Raw16<__nv_bfloat16>::pair(int i) const {
+    return make_float2(__uint_as_float(word(i) << 16), __uint_as_float(word(i) & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 Raw16<__half>::pair(int i) const {
+    const uint32_t w = word(i);
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <> __device__ __forceinline__ uint32_t Raw16<float>::magnitude(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, word(i) & 0x7fffffffu);
     return m;
 }
-
+template <> __device__ __forceinline__ uint32_t Raw16<__nv_bfloat16>::magnitude(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, word(i) & 0x7fff7fffu);
+    return m;
+}
+template <> __device__ __forceinline__ uint32_t Raw16<__half>::magnitude(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, word(i) & 0x7fff7fffu);
+    return m;
+}
+// fp32 bits of a thread's maximum
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
-    constexpr int V = Vec16<T>::N;
-#pragma unroll
-    for (int i = 0; i < 16 / V; ++i) {
-        Vec16<T> o;
-        vec_load(p + i * V, o);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[i * V + j] = o.v[j];
-    }
+__device__ __forceinline__ uint32_t magnitude_f32(uint32_t m) { return m; }
+template <>
+__device__ __forceinline__ uint32_t magnitude_f32<__nv_bfloat16>(uint32_t m) { return max(m & 0xffffu, m >> 16) << 16; }
+template <>
+__device__ __forceinline__ uint32_t magnitude_f32<__half>(uint32_t m) {
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)max(m & 0xffffu, m >> 16))));
 }
 
-// The integer nearest to the real quotient x / s, ties to even, in [-127, 127].  x * (1/s)
-// is off by less than 3e-5, so its nearest integer c is right or one off next to a tie;
-// x - c s is exact in fp32 (a multiple of an ulp of s or of x, no larger than s), and
-// comparing its double with s decides.
+// The integer nearest to the real quotient x / s, ties to even, in [-127, 127]: the
+// checked form of code_word below for one value.
 __device__ __forceinline__ int code_of(float x, float s, float inv) {
     float c = rintf(x * inv);
     const float rem = fmaf(-c, s, x);
@@ -193,30 +253,52 @@ __device__ __forceinline__ int code_of(float x, float s, float inv) {
     return (int)fminf(fmaxf(c, -127.0f), 127.0f);
 }
 
-// sx[r] = max |x[r]| * (1/127) (1 if that is zero), q = codes.  tx threads (a power of two, a
-// warp at least) share a row, which stays in registers between the two passes: NV pieces
-// of 16 values a thread.
+// Four codes in a word.  t = x / s + 1.5 2^23 rounds the quotient to an integer c whose low
+// byte is t's; x * (1/s) is off by less than 3e-5, so c is the nearest integer or one off
+// next to a tie.  x - c s is exact in fp32 (a multiple of an ulp of s or of x, no larger
+// than s): below s / 2 it proves c, and `worst` keeps the largest for that test.  Six
+// instructions a value (two values at a time in fp32x2); the tie's own test for each value
+// would take twelve, and at 6.5 TB/s a value has sixteen issue slots.
+__device__ __forceinline__ uint32_t code_word(float2 x0, float2 x1, float s, float inv, float& worst) {
+    const float magic = 12582912.0f;
+    float t0 = magic, t1 = magic, t2 = magic, t3 = magic;
+    fma2(t0, t1, x0.x, x0.y, inv, inv);
+    fma2(t2, t3, x1.x, x1.y, inv, inv);
+    float r0 = x0.x, r1 = x0.y, r2 = x1.x, r3 = x1.y;
+    fma2(r0, r1, magic - t0, magic - t1, s, s);
+    fma2(r2, r3, magic - t2, magic - t3, s, s);
+    worst = fmaxf(fmaxf(worst, fabsf(r0)), fabsf(r1));
+    worst = fmaxf(fmaxf(worst, fabsf(r2)), fabsf(r3));
+    const uint32_t lo = __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(t2), __float_as_uint(t3), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
+
+// sx[r] = max |x[r]| * (1/127) (1 if that is zero), q = codes.  tx threads (a power of two,
+// a warp at least) share a row, which stays in registers between the two passes: NV
+// pieces of 16 values a thread.
 template <typename T, int NV>
-__global__ void __launch_bounds__(512) quantize_int8_kernel(const T* __restrict__ x, long long ldx, int n, int k, const int* n_rows,
-                                     int8_t* __restrict__ q, float* __restrict__ sx, int tx) {
-    __shared__ uint32_t part[2][32];
+__global__ void __launch_bounds__(512) quantize_int8_kernel(const T* __restrict__ x, long long ldx, int n, int k,
+                                                            const int* n_rows, int8_t* __restrict__ q,
+                                                            float* __restrict__ sx, int tx) {
+    __shared__ uint32_t part[2][16];
     const int t = threadIdx.x & (tx - 1);
     const int ty = blockDim.x / tx;
     const int rows = rows_to_compute(n_rows, n);
     int flip = 0;
     for (int r0 = blockIdx.x * ty; r0 < rows; r0 += gridDim.x * ty) {
         const int r = r0 + threadIdx.x / tx;
-        float v[NV][16];
+        Raw16<T> v[NV];
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tx) * 16;
-            if (r < rows && c < k) load16(x + (size_t)r * ldx + c, v[i]);
+            if (r < rows && c < k) v[i].load(x + (size_t)r * ldx + c);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (r < rows && (t + i * tx) * 16 < k) m = abs_bits_max(m, v[i]);
-        m = __reduce_max_sync(0xffffffffu, m);
+            if (r < rows && (t + i * tx) * 16 < k) m = v[i].magnitude(m);
+        m = __reduce_max_sync(0xffffffffu, magnitude_f32<T>(m));
         if (tx > 32) {
             if ((threadIdx.x & 31) == 0) part[flip][threadIdx.x >> 5] = m;
             __syncthreads();
@@ -231,17 +313,28 @@ __global__ void __launch_bounds__(512) quantize_int8_kernel(const T* __restrict_
         // an infinity or a NaN in the row: the scale is not finite and the codes are zero
         const bool bad = !(s < __uint_as_float(0x7f800000u));
         // tiny scales: x and s times 2^64 (exact), so that 1/s and x - c s stay normal
-        const float lift = s < 0x1p-60f ? 0x1p64f : 1.0f;
+        const bool tiny = s < 0x1p-60f;
+        const float lift = tiny ? 0x1p64f : 1.0f;
         const float ss = s * lift, inv = 1.0f / ss;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tx) * 16;
             if (c >= k) continue;
-            uint32_t w[4] = {0, 0, 0, 0};
+            uint32_t w[4];
+            float worst = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int code = bad ? 0 : code_of(v[i][j] * lift, ss, inv);
-                w[j >> 2] |= (uint32_t)(code & 0xff) << (8 * (j & 3));
+            for (int j = 0; j < 4; ++j) w[j] = code_word(v[i].pair(2 * j), v[i].pair(2 * j + 1), ss, inv, worst);
+            if (bad || tiny || !(worst < 0.5f * ss)) {  // a tie or a code one off (about 1 in 10^5 values): each checked
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 a = v[i].pair(2 * j), b = v[i].pair(2 * j + 1);
+                    const float f[4] = {a.x, a.y, b.x, b.y};
+                    uint32_t u = 0;
+#pragma unroll
+                    for (int l = 0; l < 4; ++l)
+                        u |= bad ? 0u : (uint32_t)(code_of(f[l] * lift, ss, inv) & 0xff) << (8 * l);
+                    w[j] = u;
+                }
             }
             *reinterpret_cast<uint4*>(q + (size_t)r * k + c) = make_uint4(w[0], w[1], w[2], w[3]);
         }
