@@ -1427,7 +1427,7 @@ static void launch_swiglu_t(bool backward, const SwigluArgs& a, int n_sm, cudaSt
     while (tx < vecs && tx < ROWS_THREADS && (tx < 32 || (long long)a.rows * tx < (long long)n_sm * 2048)) tx *= 2;
     const int rows_per_cta = ROWS_THREADS / tx;
     const int want = (a.rows + rows_per_cta - 1) / rows_per_cta;
-    const int grid = want < n_sm * 8 ? want : n_sm * 8;
+    const int grid = want < n_sm * 16 ? want : n_sm * 16;
     note_launch();
     if (backward) swiglu_backward_kernel<T><<<grid, ROWS_THREADS, 0, s>>>(a, tx);
     else swiglu_kernel<T><<<grid, ROWS_THREADS, 0, s>>>(a, tx);
@@ -1444,8 +1444,10 @@ template <typename T>
 static void launch_quantize_t(const void* x, long long ldx, int rows, int k, const int* n_rows, int8_t* q, float* sx,
                               int n_sm, cudaStream_t s) {
     const int vecs = k / 16;
+    // Two pieces a thread (four where k > 16384: 512 threads at most); one where there are too
+    // few rows to hide a row's latency.
     int tx = 32;
-    while (tx * 4 < vecs) tx *= 2;  // at most 512: k <= 32768
+    while (tx < 512 && tx * (rows <= 2 * n_sm ? 1 : 2) < vecs) tx *= 2;
     const int ty = tx < 128 ? 128 / tx : 1;
     const int want = (rows + ty - 1) / ty;
     const int grid = want < n_sm * 16 ? want : n_sm * 16;

@@ -82,12 +82,8 @@ __device__ __forceinline__ float row_sigmoid(float z) {
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
 
-// How the row operators share out rows: tx threads (a power of two) take a row together,
-// ROWS_THREADS / tx rows a CTA, and a thread works on ROWS_BATCH 16-byte pieces at a time
-// so that their loads are under way together.
-constexpr int ROWS_BATCH = 2;
-
-// h = c * silu(gate) * up.  h may be gate or up: a thread writes only pieces it has read.
+// h = c * silu(gate) * up.  tx threads (a power of two) share a row, ROWS_THREADS / tx rows
+// a CTA.  h may be gate or up: a thread writes only pieces it has read.
 template <typename T>
 __global__ void __launch_bounds__(ROWS_THREADS) swiglu_kernel(const __grid_constant__ SwigluArgs A, int tx) {
     constexpr int V = Vec16<T>::N;
@@ -99,31 +95,23 @@ __global__ void __launch_bounds__(ROWS_THREADS) swiglu_kernel(const __grid_const
         const T* u = static_cast<const T*>(A.up) + (size_t)r * A.ld_up;
         T* h = static_cast<T*>(A.out0) + (size_t)r * A.ld_out0;
         const float c = A.coef ? A.coef[r] : 1.0f;
-        for (int i0 = t * V; i0 < A.width; i0 += ROWS_BATCH * tx * V) {
-            Vec16<T> a[ROWS_BATCH], b[ROWS_BATCH];
+        for (int i = t * V; i < A.width; i += tx * V) {
+            Vec16<T> a, b;
+            vec_load(g + i, a);
+            vec_load(u + i, b);
 #pragma unroll
-            for (int k = 0; k < ROWS_BATCH; ++k) {
-                const int i = i0 + k * tx * V;
-                if (i < A.width) {
-                    vec_load(g + i, a[k]);
-                    vec_load(u + i, b[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < ROWS_BATCH; ++k) {
-                const int i = i0 + k * tx * V;
-                if (i < A.width) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) a[k].v[j] = c * (a[k].v[j] * row_sigmoid<T>(a[k].v[j]) * b[k].v[j]);
-                    vec_store(h + i, a[k]);
-                }
-            }
+            for (int j = 0; j < V; ++j) a.v[j] = c * (a.v[j] * row_sigmoid<T>(a.v[j]) * b.v[j]);
+            vec_store(h + i, a);
         }
     }
 }
 
 // dgate = c dh up (s + silu (1 - s)), dup = c dh silu, dcoef = sum dh silu up, with
 // s = sigmoid(gate), silu = gate s.  dgate may be gate and dup may be up or dh.
+// Bound by HBM: 131072 rows of 2048 in bf16 (2.7 GB) take 419 us, 98 % of the copy rate.
+// With one warp to a row the sum needs no barrier; two, four or eight warps take 440, 450
+// and 483 us, and two or four pieces of a thread loaded together 474 and 540 us (fewer
+// warps fit).
 template <typename T>
 __global__ void __launch_bounds__(ROWS_THREADS) swiglu_backward_kernel(const __grid_constant__ SwigluArgs A, int tx) {
     constexpr int V = Vec16<T>::N;
@@ -143,34 +131,22 @@ __global__ void __launch_bounds__(ROWS_THREADS) swiglu_backward_kernel(const __g
             T* dg = static_cast<T*>(A.out0) + (size_t)r * A.ld_out0;
             T* du = static_cast<T*>(A.out1) + (size_t)r * A.ld_out1;
             const float c = A.coef ? A.coef[r] : 1.0f;
-            for (int i0 = t * V; i0 < A.width; i0 += ROWS_BATCH * tx * V) {
-                Vec16<T> a[ROWS_BATCH], b[ROWS_BATCH], e[ROWS_BATCH];
+            for (int i = t * V; i < A.width; i += tx * V) {
+                Vec16<T> a, b, e;
+                vec_load(g + i, a);
+                vec_load(u + i, b);
+                vec_load(d + i, e);
 #pragma unroll
-                for (int k = 0; k < ROWS_BATCH; ++k) {
-                    const int i = i0 + k * tx * V;
-                    if (i < A.width) {
-                        vec_load(g + i, a[k]);
-                        vec_load(u + i, b[k]);
-                        vec_load(d + i, e[k]);
-                    }
+                for (int j = 0; j < V; ++j) {
+                    const float s = row_sigmoid<T>(a.v[j]);
+                    const float act = a.v[j] * s;
+                    const float ce = c * e.v[j];
+                    dot = fmaf(e.v[j] * act, b.v[j], dot);
+                    a.v[j] = ce * b.v[j] * fmaf(act, 1.0f - s, s);
+                    b.v[j] = ce * act;
                 }
-#pragma unroll
-                for (int k = 0; k < ROWS_BATCH; ++k) {
-                    const int i = i0 + k * tx * V;
-                    if (i < A.width) {
-#pragma unroll
-                        for (int j = 0; j < V; ++j) {
-                            const float s = row_sigmoid<T>(a[k].v[j]);
-                            const float act = a[k].v[j] * s;
-                            const float ce = c * e[k].v[j];
-                            dot = fmaf(e[k].v[j] * act, b[k].v[j], dot);
-                            a[k].v[j] = ce * b[k].v[j] * fmaf(act, 1.0f - s, s);
-                            b[k].v[j] = ce * act;
-                        }
-                        vec_store(dg + i, a[k]);
-                        vec_store(du + i, b[k]);
-                    }
-                }
+                vec_store(dg + i, a);
+                vec_store(du + i, b);
             }
         }
         if (A.dcoef) {  // fixed order: lanes by a butterfly, then the row's warps one after another
@@ -276,7 +252,7 @@ __device__ __forceinline__ uint32_t code_word(float2 x0, float2 x1, float s, flo
 
 // sx[r] = max |x[r]| * (1/127) (1 if that is zero), q = codes.  tx threads (a power of two,
 // a warp at least) share a row, which stays in registers between the two passes: NV
-// pieces of 16 values a thread.
+// pieces of 16 values a thread.  Bound by HBM: 16384 rows of 7168 in bf16 (352 MB).
 template <typename T, int NV>
 __global__ void __launch_bounds__(512) quantize_int8_kernel(const T* __restrict__ x, long long ldx, int n, int k,
                                                             const int* n_rows, int8_t* __restrict__ q,
@@ -286,18 +262,24 @@ __global__ void __launch_bounds__(512) quantize_int8_kernel(const T* __restrict_
     const int ty = blockDim.x / tx;
     const int rows = rows_to_compute(n_rows, n);
     int flip = 0;
-    for (int r0 = blockIdx.x * ty; r0 < rows; r0 += gridDim.x * ty) {
-        const int r = r0 + threadIdx.x / tx;
-        Raw16<T> v[NV];
-        uint32_t m = 0;
+    Raw16<T> v[NV], next[NV];
+    auto load = [&](Raw16<T>(&d)[NV], int r) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tx) * 16;
-            if (r < rows && c < k) v[i].load(x + (size_t)r * ldx + c);
+            if (r < rows && c < k) d[i].load(x + (size_t)r * ldx + c);
         }
+    };
+    load(next, blockIdx.x * ty + threadIdx.x / tx);
+    for (int r0 = blockIdx.x * ty; r0 < rows; r0 += gridDim.x * ty) {
+        const int r = r0 + threadIdx.x / tx;
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            v[i] = next[i];
             if (r < rows && (t + i * tx) * 16 < k) m = v[i].magnitude(m);
+        }
+        load(next, r + gridDim.x * ty);  // under way while this row is worked on
         m = __reduce_max_sync(0xffffffffu, magnitude_f32<T>(m));
         if (tx > 32) {
             if ((threadIdx.x & 31) == 0) part[flip][threadIdx.x >> 5] = m;
