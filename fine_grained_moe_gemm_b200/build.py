@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
 SOURCES = ["moe_kernels.cu", "moe_api.cu", "moe_products.cu", "moe_noalloc.cu"]
-HEADERS = ["moe_device.cuh", "moe_gemm.cuh", "moe_gemm_fp8.cuh", "moe_gemm2.cuh", "moe_gemm2_fp8.cuh", "moe_ragged.cuh",
+HEADERS = ["moe_device.cuh", "moe_gemm.cuh", "moe_gemm_fp8.cuh", "moe_gemm2.cuh", "moe_gemm2_fp8.cuh", "moe_ragged.cuh", "moe_split.cuh",
            "moe_rows.cuh", "moe_host.h", "moe_launch.h", os.path.join("..", "..", "include", "moe.h")]
 
 NVCC_FLAGS = [

@@ -19,6 +19,7 @@
 //   finalize_kernel       fp32 combine buffer -> bf16 output (+ residual)
 //   moe_ragged_kernel     products grouped by expert: projections, input and weight
 //                         gradients, 8-bit integers (moe_ragged.cuh)
+//   moe_split_kernel      the same where they have few tiles (moe_split.cuh)
 //   swiglu_kernel, swiglu_backward_kernel, quantize_int8_kernel  row operators (moe_rows.cuh)
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -36,6 +37,7 @@
 #include "moe_launch.h"
 #include "moe_ragged.cuh"
 #include "moe_rows.cuh"
+#include "moe_split.cuh"
 
 namespace moe {
 
@@ -1415,6 +1417,44 @@ cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cu
     if (dir != RAG_TN) return cudaErrorInvalidValue;
     return promote ? launch_ragged_t<RAG_TN, false, true>(args, grid, s)
                    : launch_ragged_t<RAG_TN, false, false>(args, grid, s);
+}
+
+template <int DIR, bool I8>
+static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_t s) {
+    auto kernel = moe_split_kernel<DIR, I8>;
+    constexpr int most = 227 * 1024;
+    static std::atomic<bool> attr_set[64];  // once per device (a repeated set is harmless)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
+    }
+    args->stages = SPLIT_MAX_STAGES;
+    while (split_smem_bytes(args->bn, args->stages) > most) --args->stages;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = args->split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * args->split));
+    cfg.blockDim = dim3(SPLIT_THREADS);
+    cfg.dynamicSmemBytes = split_smem_bytes(args->bn, args->stages);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, (const RaggedArgs)*args);
+}
+
+cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s) {
+    if (tiles < 1 || args->split < 1 || args->split > SPLIT_MAX_CLUSTER || tiles * args->split > (1 << 30))
+        return cudaErrorInvalidValue;
+    if (i8) return dir == RAG_NT ? launch_split_t<RAG_NT, true>(args, tiles, s) : cudaErrorInvalidValue;
+    if (dir == RAG_NT) return launch_split_t<RAG_NT, false>(args, tiles, s);
+    if (dir == RAG_NN) return launch_split_t<RAG_NN, false>(args, tiles, s);
+    return dir == RAG_TN ? launch_split_t<RAG_TN, false>(args, tiles, s) : cudaErrorInvalidValue;
 }
 
 template <typename T>

@@ -179,9 +179,15 @@ struct RaggedArgs {
     int accumulate;
     const float* sx;       // 8-bit operands: scale of each row, and of each [group][n]
     const float* sw;
+    // moe_split_kernel (b64 is then its only map of the rows, in boxes of bn rows; TN 64 x 64)
+    int bn;      // columns of a tile: 16, 32, 64 or 128 (TN: 64 or 128)
+    int split;   // CTAs that share a tile's summed axis
+    int stages;  // of the ring
 };
 
+constexpr int SPLIT_MAX_CLUSTER = 8;
 cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s);
+cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s);
 
 // ---------------------------------------------------------------- rows (moe_rows.cuh)
 struct SwigluArgs {

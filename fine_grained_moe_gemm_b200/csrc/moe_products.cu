@@ -57,10 +57,56 @@ CUtensorMapDataType map_type(moe_dtype t) {
     return t == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// CTAs of a launch: a pair for every SM pair, or fewer when the groups cannot have more items.
-int grid_of(const DevInfo& di, long long most_items) {
-    const long long want = 2 * most_items;
-    return (int)(want < (di.sm_count & ~1) ? want : (di.sm_count & ~1));
+// Which kernel runs a product, from what the host knows: the sizes, not the offsets.
+//
+// pair: moe_ragged_kernel, tiles of 256 x 256 on CTA pairs, or moe_split_kernel, tiles of
+// 128 x bn on single CTAs with the summed axis over up to eight of them.  The split kernel
+// runs where a quarter of the SMs or less would have a tile of their pair: its tiles are a
+// quarter as large and its MMAs at most 80 % as fast, so it wins by its number of CTAs.
+struct ProductPlan {
+    bool pair;
+    int grid;         // pair: CTAs
+    int bn, split;    // split kernel
+    long long tiles;  // split kernel: at most
+};
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// groups of a NT / NN product that can have rows, and chunks of at most w rows they can have
+long long chunks_of(int groups, int rows, int w) {
+    return groups == 1 ? ceil_div(rows, w) : rows / w + (groups < rows ? groups : rows);
+}
+
+ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, int n_sm) {
+    ProductPlan p = {};
+    const long long items = dir == RAG_TN ? groups * ceil_div(n, 256) * ceil_div(k, 256)
+                                          : chunks_of(groups, rows, 256) * ceil_div(n, 256);
+    const int sms = n_sm & ~1;
+    if (4 * items > sms) {
+        p.pair = true;
+        p.grid = (int)(2 * items < sms ? 2 * items : sms);
+        return p;
+    }
+    const long long mean = ceil_div(rows, groups < rows ? groups : rows);  // rows of a group that has some
+    if (dir == RAG_TN) {
+        p.bn = groups * ceil_div(n, 128) * ceil_div(k, 128) * SPLIT_MAX_CLUSTER >= sms ? 128 : 64;
+        p.tiles = groups * ceil_div(n, 128) * ceil_div(k, p.bn);
+    } else {
+        p.bn = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+        p.tiles = chunks_of(groups, rows, p.bn) * ceil_div(n, 128);
+    }
+    // parts of at least four blocks of 128 bytes (64 rows): a shorter one is over before its pipeline is full
+    const long long blocks = dir == RAG_TN ? ceil_div(mean, 64) : ceil_div(k, i8 ? 128 : 64);
+    long long split = sms / p.tiles;
+    if (split > blocks / 4) split = blocks / 4;
+    p.split = (int)(split < 1 ? 1 : split > SPLIT_MAX_CLUSTER ? SPLIT_MAX_CLUSTER : split);
+    return p;
+}
+
+moe_status run_product(int dir, bool i8, RaggedArgs* a, const ProductPlan& p, cudaStream_t s) {
+    a->bn = p.bn;
+    a->split = p.split;
+    return cuda_status(p.pair ? launch_ragged(dir, i8, a, p.grid, s) : launch_split(dir, i8, a, p.tiles, s));
 }
 
 moe_status product(bool i8, moe_dtype t, int groups, int rows, int n, int k, const void* x, int64_t ldx, const void* w,
@@ -73,11 +119,16 @@ moe_status product(bool i8, moe_dtype t, int groups, int rows, int n, int k, con
     memset(&a, 0, sizeof(a));
     const int elem = i8 ? 1 : 2;
     const CUtensorMapDataType dt = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : map_type(t);
-    const bool ok = (transpose_w ? map_box(&a.a, dt, elem, w, groups, k, n, n, 64)
-                                 : map_box(&a.a, dt, elem, w, groups, n, k, k, 128)) &&
-                    map_box(&a.b128, dt, elem, x, 0, rows, k, ldx, 128) &&
-                    map_box(&a.b64, dt, elem, x, 0, rows, k, ldx, 64) &&
-                    map_box(&a.b16, dt, elem, x, 0, rows, k, ldx, 16);
+    const int dir = transpose_w ? RAG_NN : RAG_NT;
+    const ProductPlan plan = plan_product(dir, i8, groups, rows, n, k, di.sm_count);
+    bool ok = transpose_w ? map_box(&a.a, dt, elem, w, groups, k, n, n, 64)
+                          : map_box(&a.a, dt, elem, w, groups, n, k, k, 128);
+    if (plan.pair) {
+        ok = ok && map_box(&a.b128, dt, elem, x, 0, rows, k, ldx, 128) &&
+             map_box(&a.b64, dt, elem, x, 0, rows, k, ldx, 64) && map_box(&a.b16, dt, elem, x, 0, rows, k, ldx, 16);
+    } else {
+        ok = ok && map_box(&a.b64, dt, elem, x, 0, rows, k, ldx, plan.bn);
+    }
     if (!ok) return MOE_ERR_CUDA;
     a.offsets = offsets;
     a.groups = groups;
@@ -91,8 +142,7 @@ moe_status product(bool i8, moe_dtype t, int groups, int rows, int n, int k, con
     a.accumulate = accumulate;
     a.sx = sx;
     a.sw = sw;
-    const long long items = (long long)((n + 255) / 256) * (rows / 256 + (groups < rows ? groups : rows));
-    return cuda_status(launch_ragged(transpose_w ? RAG_NN : RAG_NT, i8, &a, grid_of(di, items), (cudaStream_t)stream));
+    return run_product(dir, i8, &a, plan, (cudaStream_t)stream);
 }
 
 }  // namespace
@@ -158,8 +208,7 @@ moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dtype dtype
     a.y = dw;
     a.out = dw_dtype;
     a.accumulate = accumulate;
-    const long long items = (long long)groups * ((n + 255) / 256) * ((k + 255) / 256);
-    return cuda_status(launch_ragged(RAG_TN, false, &a, grid_of(di, items), (cudaStream_t)stream));
+    return run_product(RAG_TN, false, &a, plan_product(RAG_TN, false, groups, rows, n, k, di.sm_count), (cudaStream_t)stream);
 }
 
 moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* gate, int64_t ld_gate, const void* up,

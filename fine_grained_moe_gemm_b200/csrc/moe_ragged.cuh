@@ -90,12 +90,14 @@ __device__ __forceinline__ int rag_items_of(const RaggedArgs& P, int rows) {
     return mt * (DIR == RAG_TN ? (P.k + 255) >> 8 : (rows + 255) >> 8);
 }
 
-// Fills the table from the offsets (all threads of the CTA).  A group whose offsets
-// decrease or leave [0, rows] has no rows and sets MOE_DEVERR_BAD_ROWS.
-template <int DIR>
-__device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTable& t, int* warp_sums) {
+// Fills the table from the offsets (all THREADS threads of the CTA; the caller
+// synchronises).  A group whose offsets decrease or leave [0, rows] has no rows and sets
+// MOE_DEVERR_BAD_ROWS.
+template <int THREADS, typename ItemsOf>
+__device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTable& t, int* warp_sums,
+                                                ItemsOf items_of) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (P.groups + RAG_THREADS - 1) / RAG_THREADS;  // consecutive groups of a thread
+    const int per = (P.groups + THREADS - 1) / THREADS;  // consecutive groups of a thread
     const int g0 = tid * per;
     int sum = 0;
     for (int g = g0; g < min(g0 + per, P.groups); ++g) {
@@ -111,7 +113,7 @@ __device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTa
         t.start[g] = a;
         t.count[g] = b - a;
         t.first[g] = sum;  // within the thread, for now
-        sum += rag_items_of<DIR>(P, b - a);
+        sum += items_of(b - a);
     }
     int incl = sum;
 #pragma unroll
@@ -124,7 +126,18 @@ __device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTa
     int base = incl - sum;
     for (int w = 0; w < warp; ++w) base += warp_sums[w];
     for (int g = g0; g < min(g0 + per, P.groups); ++g) t.first[g] += base;
-    if (tid == RAG_THREADS - 1) t.first[P.groups] = base + sum;
+    if (tid == THREADS - 1) t.first[P.groups] = base + sum;
+}
+
+// The group of item i: the largest g with first[g] <= i.
+__device__ __forceinline__ int rag_group(const RagTable& t, int groups, int i) {
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= i) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
 }
 
 // Item i: the group by bisection, then inside it bands of RAG_BAND chunks (TN: column
@@ -132,12 +145,7 @@ __device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTa
 // pairs work on a block of about RAG_BAND chunks x 9 tiles whose operands L2 holds.
 template <int DIR>
 __device__ __forceinline__ RagItem rag_item(const RaggedArgs& P, const RagTable& t, int i) {
-    int lo = 0, hi = P.groups - 1;  // largest g with first[g] <= i
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.first[mid] <= i) lo = mid;
-        else hi = mid - 1;
-    }
+    const int lo = rag_group(t, P.groups, i);
     RagItem it;
     it.g = lo;
     it.row0 = t.start[lo];
@@ -194,10 +202,10 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
 // Instruction descriptor: kind::f16 (fp32 sums; `fmt` 0 = f16, 1 = bf16) or kind::i8
 // (32-bit sums of signed 8-bit operands); bits 15 / 16 say that A / B is MN-major.
 template <int DIR, bool I8>
-__device__ __forceinline__ uint32_t rag_idesc(uint32_t fmt, uint32_t N) {
+__device__ __forceinline__ uint32_t rag_idesc(uint32_t fmt, uint32_t M, uint32_t N) {
     const uint32_t d_fmt = I8 ? 2u : 1u, ab = I8 ? 1u : fmt;
     return (d_fmt << 4) | (ab << 7) | (ab << 10) | (DIR != RAG_NT ? 1u << 15 : 0u) | (DIR == RAG_TN ? 1u << 16 : 0u) |
-           ((N >> 3) << 17) | ((256u >> 4) << 24);
+           ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 __device__ __forceinline__ void mma2_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -481,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
         fence_mbar_init();
     }
     if (warp == 4) tmem_alloc_pair(tmem_slot);
-    rag_build_table<DIR>(P, tab, warp_sums);
+    rag_build_table<RAG_THREADS>(P, tab, warp_sums, [&](int rows) { return rag_items_of<DIR>(P, rows); });
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated
@@ -573,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                     // elements of the summed axis in the last block (TN: rows past it are zero up to a
                     // multiple of 16; NT, NN: the loads filled in zeros)
                     const int last = (DIR == RAG_TN ? it.rows : P.k) - (blocks - 1) * 4 * per_step;
-                    const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, (uint32_t)rag_mma_n<DIR>(it));
+                    const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, 256, (uint32_t)rag_mma_n<DIR>(it));
                     for (int kb0 = 0; kb0 < blocks; kb0 += PROMOTE ? seg_blocks : blocks) {
                         const int kb1 = PROMOTE ? min(kb0 + seg_blocks, blocks) : blocks;
                         if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) { ok = false; break; }

@@ -95,7 +95,7 @@ def _mm_case(sizes, n, k, dtype, out, transpose, seed=0, first=0, spare=0, strid
 
 
 @pytest.mark.parametrize("transpose", [False, True])
-@pytest.mark.parametrize("n,k", [(8, 8), (64, 64), (136, 72), (264, 1160), (512, 256), (1032, 200)])
+@pytest.mark.parametrize("n,k", [(8, 8), (64, 64), (136, 72), (264, 1160), (512, 256), (1032, 200), (1040, 8)])
 @pytest.mark.parametrize("sizes", [FEW, RAGGED])
 def test_mm_sizes(sizes, n, k, transpose):
     _mm_case(sizes, n, k, BF, FS, transpose, seed=n + k)
@@ -104,9 +104,10 @@ def test_mm_sizes(sizes, n, k, transpose):
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("strided", [False, True])
 @pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n", [152, 1048])   # few tiles, and enough for every SM
 @pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, FS), (FH, FH), (FH, FS)])
-def test_mm_types(dtype, out, accumulate, strided, transpose):
-    _mm_case(RAGGED, 152, 328, dtype, out, transpose, seed=7, first=5, spare=9, strided=strided, accumulate=accumulate)
+def test_mm_types(dtype, out, n, accumulate, strided, transpose):
+    _mm_case(RAGGED, n, 328, dtype, out, transpose, seed=7, first=5, spare=9, strided=strided, accumulate=accumulate)
 
 
 @pytest.mark.parametrize("sizes", [[1], [5], [300], [0, 0, 0, 1000], [1] * 300, [0] * 1023 + [2], [2049, 0, 1]])
@@ -167,15 +168,17 @@ def test_wgrad_sizes(sizes, n, k):
 
 @pytest.mark.parametrize("strided", [False, True])
 @pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n", [152, 1048])
 @pytest.mark.parametrize("dtype,out", [(BF, BF), (BF, FS), (FH, FH), (FH, FS)])
-def test_wgrad_types(dtype, out, accumulate, strided):
-    _wgrad_case(RAGGED, 152, 328, dtype, out, seed=11, first=3, spare=70, strided=strided, accumulate=accumulate)
+def test_wgrad_types(dtype, out, n, accumulate, strided):
+    _wgrad_case(RAGGED, n, 328, dtype, out, seed=11, first=3, spare=70, strided=strided, accumulate=accumulate)
 
 
+@pytest.mark.parametrize("n", [136, 1032])
 @pytest.mark.parametrize("poison", [3, 9, 11])
-def test_wgrad_neighbours_do_not_leak(poison):
+def test_wgrad_neighbours_do_not_leak(poison, n):
     """A group of NaN and infinities lies right behind another group's last rows, inside its 64-row block."""
-    _wgrad_case(RAGGED, 136, 136, BF, FS, seed=12, poison=poison)
+    _wgrad_case(RAGGED, n, 136, BF, FS, seed=12, poison=poison)
 
 
 @pytest.mark.parametrize("dtype", [BF, FH])
@@ -199,17 +202,33 @@ def test_long_fp32_sums_keep_their_precision(dtype):
     assert moe.device_error() == 0
 
 
+@pytest.mark.parametrize("n", [136, 1032])   # few tiles, and enough for every SM
 @pytest.mark.parametrize("transpose", [False, True])
 @pytest.mark.parametrize("strided", [False, True])
-def test_long_fp32_sums_ragged(transpose, strided):
-    _mm_case(RAGGED, 136, 1048, BF, FS, transpose, seed=31, first=2, spare=3, strided=strided, accumulate=True)
+def test_long_fp32_sums_ragged(transpose, strided, n):
+    _mm_case(RAGGED, n, 1048, BF, FS, transpose, seed=31, first=2, spare=3, strided=strided, accumulate=True)
 
 
+@pytest.mark.parametrize("n", [136, 1032])
 @pytest.mark.parametrize("accumulate", [False, True])
-def test_long_fp32_gradients_ragged(accumulate):
-    _wgrad_case([0, 700, 3, 1500, 0, 512, 513, 1025], 136, 264, BF, FS, seed=32, first=1, spare=5, accumulate=accumulate,
+def test_long_fp32_gradients_ragged(accumulate, n):
+    _wgrad_case([0, 700, 3, 1500, 0, 512, 513, 1025], n, 264, BF, FS, seed=32, first=1, spare=5, accumulate=accumulate,
                 poison=4)
-    _wgrad_case([700, 3, 1500], 136, 264, FH, FS, seed=33, accumulate=accumulate, poison=1)
+    _wgrad_case([700, 3, 1500], n, 264, FH, FS, seed=33, accumulate=accumulate, poison=1)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 33, 63, 65, 128, 129, 300])
+@pytest.mark.parametrize("n,k", [(8, 8), (136, 2056), (264, 18432)])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_mm_one_group_of_few_rows(rows, n, k, transpose):
+    """Few tiles over a long axis: the axis is shared by up to eight CTAs."""
+    _mm_case([rows], n, k, BF, BF if rows % 2 else FS, transpose, seed=rows, first=3, spare=2, accumulate=rows % 3 == 0)
+
+
+@pytest.mark.parametrize("rows", [1, 15, 16, 63, 64, 65, 257, 1000, 4099])
+@pytest.mark.parametrize("n,k", [(8, 8), (72, 136), (136, 264)])
+def test_wgrad_one_group_of_few_tiles(rows, n, k):
+    _wgrad_case([rows], n, k, FH, FH if rows % 2 else FS, seed=rows, first=1, spare=70, accumulate=rows % 3 == 0)
 
 
 def test_wgrad_without_rows_is_zero():
@@ -300,7 +319,8 @@ def _codes(gen, shape):
 
 @pytest.mark.parametrize("out", [BF, FH, FS])
 @pytest.mark.parametrize("accumulate", [False, True])
-@pytest.mark.parametrize("sizes,n,k", [(FEW, 8, 16), (RAGGED, 136, 80), (RAGGED, 264, 1168), ([16], 1032, 2064),
+@pytest.mark.parametrize("sizes,n,k", [(FEW, 8, 16), (RAGGED, 136, 80), (RAGGED, 264, 1168), (RAGGED, 1032, 208), ([16], 1032, 2064),
+                                       ([16], 136, 18432),
                                        ([300], 256, 128), ([0] * 200 + [1], 64, 32), ([2], 16, 65536)])
 def test_mm_int8(sizes, n, k, accumulate, out):
     gen = _gen(n + k)
