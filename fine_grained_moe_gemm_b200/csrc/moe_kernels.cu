@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "moe_device.cuh"
 #include "moe_gemm.cuh"
@@ -1428,6 +1429,7 @@ static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
     }
@@ -1446,6 +1448,37 @@ static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_
     cfg.numAttrs = 1;
     note_launch();
     return cudaLaunchKernelEx(&cfg, kernel, (const RaggedArgs)*args);
+}
+
+int split_clusters(int split) {
+    static std::mutex mu;
+    static int known[64][SPLIT_MAX_CLUSTER + 1];  // count + 1; 0: not asked yet
+    int dev = 0;
+    if (split < 1 || split > SPLIT_MAX_CLUSTER || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int& have = known[dev][split];
+    if (!have) {  // one CTA an SM: every variant takes more than half of the shared memory
+        auto kernel = moe_split_kernel<RAG_NT, false>;
+        int n = 0;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = split;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(split);
+        cfg.blockDim = dim3(SPLIT_THREADS);
+        cfg.dynamicSmemBytes = 227 * 1024;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();  // this size is not used
+            n = 0;
+        }
+        have = n + 1;
+    }
+    return have - 1;
 }
 
 cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s) {

@@ -179,13 +179,15 @@ struct RaggedArgs {
     int accumulate;
     const float* sx;       // 8-bit operands: scale of each row, and of each [group][n]
     const float* sw;
+    int bn;      // columns of a tile: 256 or 128; moe_split_kernel: 128, 64, 32 or 16 (TN: 128 or 64)
     // moe_split_kernel (b64 is then its only map of the rows, in boxes of bn rows; TN 64 x 64)
-    int bn;      // columns of a tile: 16, 32, 64 or 128 (TN: 64 or 128)
     int split;   // CTAs that share a tile's summed axis
     int stages;  // of the ring
 };
 
-constexpr int SPLIT_MAX_CLUSTER = 8;
+constexpr int SPLIT_MAX_CLUSTER = 16;
+// Clusters of `split` CTAs that run at the same time on the current device (0: none)
+int split_clusters(int split);
 cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s);
 cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s);
 

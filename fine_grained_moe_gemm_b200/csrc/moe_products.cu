@@ -16,6 +16,8 @@ namespace {
 constexpr int kMaxWidth = 65536;     // n, k: 128 * 128 * 65536 = 2^30, so 8-bit sums stay inside 32 bits
 constexpr int kMaxRows = 1 << 24;    // items of all groups stay inside 32 bits
 constexpr int kMaxQuantWidth = 32768;  // a row in registers: 512 threads of four 16-value pieces
+// clocks of a tile besides its blocks, and of the meeting of a split tile's parts
+constexpr int kTileClocks = 2500, kMeetClocks = 2500;
 constexpr int64_t kMaxLd = 1ll << 36;
 
 int size_of(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
@@ -59,48 +61,57 @@ CUtensorMapDataType map_type(moe_dtype t) {
 
 // Which kernel runs a product, from what the host knows: the sizes, not the offsets.
 //
-// pair: moe_ragged_kernel, tiles of 256 x 256 on CTA pairs, or moe_split_kernel, tiles of
-// 128 x bn on single CTAs with the summed axis over up to eight of them.  The split kernel
-// runs where a quarter of the SMs or less would have a tile of their pair: its tiles are a
-// quarter as large and its MMAs at most 80 % as fast, so it wins by its number of CTAs.
+// pair: moe_ragged_kernel, tiles of 256 features x bn columns on CTA pairs; else
+// moe_split_kernel, tiles of 128 x bn on single CTAs with the summed axis over `split` of
+// them.  Both take a block of 128 bytes of the summed axis at a time, and a CTA gets about
+// 45 bytes a clock into shared memory, so a block of a tile with c columns a CTA costs
+// (128 + c) * 128 / 45 clocks, and a product its rounds of tiles times its blocks.  The
+// cheapest of the choices runs; a split also pays for its meeting.
 struct ProductPlan {
     bool pair;
     int grid;         // pair: CTAs
-    int bn, split;    // split kernel
+    int bn, split;
     long long tiles;  // split kernel: at most
 };
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// groups of a NT / NN product that can have rows, and chunks of at most w rows they can have
+// chunks of at most w rows that the groups of a NT / NN product can have
 long long chunks_of(int groups, int rows, int w) {
     return groups == 1 ? ceil_div(rows, w) : rows / w + (groups < rows ? groups : rows);
 }
 
 ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, int n_sm) {
-    ProductPlan p = {};
-    const long long items = dir == RAG_TN ? groups * ceil_div(n, 256) * ceil_div(k, 256)
-                                          : chunks_of(groups, rows, 256) * ceil_div(n, 256);
     const int sms = n_sm & ~1;
-    if (4 * items > sms) {
-        p.pair = true;
-        p.grid = (int)(2 * items < sms ? 2 * items : sms);
-        return p;
-    }
     const long long mean = ceil_div(rows, groups < rows ? groups : rows);  // rows of a group that has some
-    if (dir == RAG_TN) {
-        p.bn = groups * ceil_div(n, 128) * ceil_div(k, 128) * SPLIT_MAX_CLUSTER >= sms ? 128 : 64;
-        p.tiles = groups * ceil_div(n, 128) * ceil_div(k, p.bn);
-    } else {
-        p.bn = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
-        p.tiles = chunks_of(groups, rows, p.bn) * ceil_div(n, 128);
-    }
-    // parts of at least four blocks of 128 bytes (64 rows): a shorter one is over before its pipeline is full
     const long long blocks = dir == RAG_TN ? ceil_div(mean, 64) : ceil_div(k, i8 ? 128 : 64);
-    long long split = sms / p.tiles;
-    if (split > blocks / 4) split = blocks / 4;
-    p.split = (int)(split < 1 ? 1 : split > SPLIT_MAX_CLUSTER ? SPLIT_MAX_CLUSTER : split);
-    return p;
+    ProductPlan best = {};
+    long long best_cost = -1;
+    auto offer = [&](bool pair, int bn, int split, long long tiles, long long at_once, long long extra) {
+        const long long cost =
+            ceil_div(tiles, at_once) * (ceil_div(blocks, split) * ((128 + (pair ? bn / 2 : bn)) * 128 / 45) + kTileClocks + extra);
+        if (best_cost >= 0 && cost >= best_cost) return;
+        best_cost = cost;
+        best.pair = pair;
+        best.bn = bn;
+        best.split = split;
+        best.tiles = tiles;
+        best.grid = (int)(2 * tiles < sms ? 2 * tiles : sms);
+    };
+    auto columns = [&](int bn) { return dir == RAG_TN ? groups * ceil_div(k, bn) : chunks_of(groups, rows, bn); };
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        offer(true, bn, 1, columns(bn) * ceil_div(n, 256), sms / 2, 0);
+        if (2 * best.tiles >= 4 * sms) return best;  // rounds enough for their rest not to matter
+    }
+    for (int bn = 128; bn >= (dir == RAG_TN ? 64 : 16); bn /= 2) {
+        const long long tiles = columns(bn) * ceil_div(n, 128);
+        // parts of four blocks at least: a shorter one is over before its pipeline is full
+        for (int split = 1; split <= SPLIT_MAX_CLUSTER && (split == 1 || 4 * split <= blocks); ++split) {
+            const int at_once = split_clusters(split);
+            if (at_once > 0) offer(false, bn, split, tiles, at_once, split > 1 ? kMeetClocks : 0);
+        }
+    }
+    return best;
 }
 
 moe_status run_product(int dir, bool i8, RaggedArgs* a, const ProductPlan& p, cudaStream_t s) {

@@ -10,8 +10,8 @@
 // Tiling.  The output's feature axis n is M of the tensor-core tile (256 per CTA
 // pair, 128 per SM), the ragged row axis (TN: the k axis) is N, up to 256 wide.  A
 // group's rows then cost MMA width only in steps of 32, where rows as M would pad
-// every group to 128 or 256 of them.  A group of more than 256 rows is cut into
-// equal chunks.  Each SM loads its own 128 features and half of the chunk's rows.
+// every group to 128 or 256 of them.  A group of more than P.bn rows (256, or 128 where
+// the product has too few tiles for every SM) is cut into equal chunks.  Each SM loads its own 128 features and half of the chunk's rows.
 // An accumulator is 256 TMEM columns, so two fit: the epilogue of one item overlaps
 // the products of the next.
 //
@@ -83,11 +83,14 @@ struct RagTable {
     int* first;   // [groups + 1] first item
 };
 
-// Items of a group of `rows` rows.
+// Chunks of a group of `rows` rows (TN: column tiles of its dw), and its items.
+template <int DIR>
+__device__ __forceinline__ int rag_chunks(const RaggedArgs& P, int rows) {
+    return ((DIR == RAG_TN ? P.k : rows) + P.bn - 1) / P.bn;
+}
 template <int DIR>
 __device__ __forceinline__ int rag_items_of(const RaggedArgs& P, int rows) {
-    const int mt = (P.n + 255) >> 8;
-    return mt * (DIR == RAG_TN ? (P.k + 255) >> 8 : (rows + 255) >> 8);
+    return ((P.n + 255) >> 8) * rag_chunks<DIR>(P, rows);
 }
 
 // Fills the table from the offsets (all THREADS threads of the CTA; the caller
@@ -151,7 +154,7 @@ __device__ __forceinline__ RagItem rag_item(const RaggedArgs& P, const RagTable&
     it.row0 = t.start[lo];
     it.rows = t.count[lo];
     const int mt = (P.n + 255) >> 8;
-    const int nc = DIR == RAG_TN ? (P.k + 255) >> 8 : (it.rows + 255) >> 8;
+    const int nc = rag_chunks<DIR>(P, it.rows);
     int local = i - t.first[lo];
     const int band = local / (RAG_BAND * mt);
     local -= band * RAG_BAND * mt;
@@ -160,10 +163,10 @@ __device__ __forceinline__ RagItem rag_item(const RaggedArgs& P, const RagTable&
     const int c = band * RAG_BAND + local - it.m * nb;
     it.chunks = nc;
     if (DIR == RAG_TN) {
-        it.col0 = c * 256;
-        it.width = min(256, P.k - it.col0);
+        it.col0 = c * P.bn;
+        it.width = min(P.bn, P.k - it.col0);
     } else {
-        const int w = ((it.rows + nc - 1) / nc + 31) & ~31;  // equal chunks, at most 256 rows
+        const int w = ((it.rows + nc - 1) / nc + 31) & ~31;  // equal chunks, at most bn rows
         it.col0 = 0;
         it.row0 += c * w;
         it.width = min(w, it.rows - c * w);
@@ -686,11 +689,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
             const int f0 = it.m * 256 + (int)rank * 128 + q * 32;
             const size_t base = (size_t)it.g * P.n * P.k;  // TN: the group's dw
             if (DIR == RAG_TN && it.rows == 0) {
-                if (!P.accumulate && f0 + lane < P.n) {
-                    uint8_t* row = static_cast<uint8_t*>(P.y) +
-                                   (base + (size_t)(f0 + lane) * P.k + it.col0) * (P.out == MOE_F32 ? 4 : 2);
-                    const int pieces = it.width * (P.out == MOE_F32 ? 4 : 2) / 16;  // k is a multiple of 8
-                    for (int p = half; p < pieces; p += 2) reinterpret_cast<uint4*>(row)[p] = make_uint4(0, 0, 0, 0);
+                if (!P.accumulate) {  // zeros, a row of the warp's 32 after the other; k is a multiple of 8
+                    const int e = P.out == MOE_F32 ? 4 : 2, pieces = it.width * e / 16;
+                    for (int r = 0; r < min(32, P.n - f0); ++r) {
+                        uint4* row = reinterpret_cast<uint4*>(static_cast<uint8_t*>(P.y) +
+                                                              (base + (size_t)(f0 + r) * P.k + it.col0) * e);
+                        for (int p = 32 * half + lane; p < pieces; p += 64) row[p] = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 continue;
             }

@@ -2,7 +2,7 @@
 // rows, narrow outputs, or a weight gradient of few tiles over many rows.
 //
 // Tiles are smaller (128 features by P.bn <= 128 columns, one CTA each) and the summed
-// axis is cut over the P.split CTAs of a cluster, one tile a cluster.  Each CTA sums its
+// axis is cut over the P.split <= 16 CTAs of a cluster, one tile a cluster.  Each CTA sums its
 // part; the parts meet through distributed shared memory: after a cluster barrier CTA s
 // adds its share of the tile's rows over all parts, in the parts' order, and stores it.
 // No workspace, no atomics, the same result every time.
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     constexpr int seg_blocks = I8 ? 1 << 30 : RAG_SEGMENT / 64;
     const int len = DIR == RAG_TN ? rows : P.k;
     const int all_blocks = work && width > 0 ? (len + block_k - 1) / block_k : 0;
-    const int kb0 = (int)((long long)all_blocks * rank / P.split), kb1 = (int)((long long)all_blocks * (rank + 1) / P.split);
+    auto split_begin = [&](int blocks, int part) { return (int)((unsigned)blocks * (unsigned)part / (unsigned)P.split); };
+    const int kb0 = split_begin(all_blocks, rank), kb1 = split_begin(all_blocks, rank + 1);
     const int mma_n = DIR == RAG_TN ? (width + 63) & ~63 : (width + 15) & ~15;
 
     float sum[2][32];  // this thread's feature, columns 32 (half + 2 c) + j; integers as bits
@@ -329,22 +330,29 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
         const int n_vec = (DIR == RAG_TN ? width : min(128, P.n - f0)) / 4;  // its pieces of four
         const int pitch = DIR == RAG_TN ? bn + 4 : 128;
         const int r0 = n_rows * rank / P.split, r1 = n_rows * (rank + 1) / P.split;
-        const int parts = min(P.split, all_blocks);
         for (int i = t; i < (r1 - r0) * n_vec; i += SPLIT_EPI_WARPS * 32) {
             const int r = r0 + i / n_vec, v = i % n_vec;
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             int4 z = make_int4(0, 0, 0, 0);
-            for (int p = 0; p < P.split; ++p) {
-                // parts without blocks (fewer blocks than CTAs) hold nothing
-                if (parts < P.split && (long long)all_blocks * p / P.split == (long long)all_blocks * (p + 1) / P.split) continue;
-                const float4 u = ld_cluster_f4(mapa_shared(part + (uint32_t)(r * pitch + v * 4) * 4, (uint32_t)p));
-                if (I8) {
-                    z.x += __float_as_int(u.x);
-                    z.y += __float_as_int(u.y);
-                    z.z += __float_as_int(u.z);
-                    z.w += __float_as_int(u.w);
-                } else {
-                    s = make_float4(s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w);
+            for (int p0 = 0; p0 < P.split; p0 += 8) {
+                float4 u[8];  // loads of eight parts under way together
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    u[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    // parts without blocks (fewer blocks than CTAs) hold nothing
+                    if (p0 + p < P.split && split_begin(all_blocks, p0 + p) < split_begin(all_blocks, p0 + p + 1))
+                        u[p] = ld_cluster_f4(mapa_shared(part + (uint32_t)(r * pitch + v * 4) * 4, (uint32_t)(p0 + p)));
+                }
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    if (I8) {
+                        z.x += __float_as_int(u[p].x);
+                        z.y += __float_as_int(u[p].y);
+                        z.z += __float_as_int(u[p].z);
+                        z.w += __float_as_int(u[p].w);
+                    } else {
+                        s = make_float4(s.x + u[p].x, s.y + u[p].y, s.z + u[p].z, s.w + u[p].w);
+                    }
                 }
             }
             if (DIR == RAG_TN) {
