@@ -28,7 +28,6 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "moe_device.cuh"
 #include "moe_gemm.cuh"
@@ -1451,12 +1450,10 @@ static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_
 }
 
 int split_clusters(int split) {
-    static std::mutex mu;
-    static int known[64][SPLIT_MAX_CLUSTER + 1];  // count + 1; 0: not asked yet
+    static std::atomic<int> known[64][SPLIT_MAX_CLUSTER + 1];  // count + 1; 0: not asked yet
     int dev = 0;
     if (split < 1 || split > SPLIT_MAX_CLUSTER || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    int& have = known[dev][split];
+    int have = known[dev][split].load(std::memory_order_relaxed);
     if (!have) {  // one CTA an SM: every variant takes more than half of the shared memory
         auto kernel = moe_split_kernel<RAG_NT, false>;
         int n = 0;
@@ -1477,6 +1474,7 @@ int split_clusters(int split) {
             n = 0;
         }
         have = n + 1;
+        known[dev][split].store(have, std::memory_order_relaxed);
     }
     return have - 1;
 }

@@ -16,8 +16,9 @@ namespace {
 constexpr int kMaxWidth = 65536;     // n, k: 128 * 128 * 65536 = 2^30, so 8-bit sums stay inside 32 bits
 constexpr int kMaxRows = 1 << 24;    // items of all groups stay inside 32 bits
 constexpr int kMaxQuantWidth = 32768;  // a row in registers: 512 threads of four 16-value pieces
-// clocks of a tile besides its blocks, and of the meeting of a split tile's parts
-constexpr int kTileClocks = 2500, kMeetClocks = 2500;
+// Clocks besides the blocks': of a pair kernel's launch and of each of its tiles, of each
+// round of the split kernel (whose CTAs start anew for every tile), of the meeting of parts.
+constexpr int kPairClocks = 6000, kPairTileClocks = 2500, kSplitTileClocks = 8500, kMeetClocks = 1500;
 constexpr int64_t kMaxLd = 1ll << 36;
 
 int size_of(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
@@ -84,13 +85,14 @@ long long chunks_of(int groups, int rows, int w) {
 ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, int n_sm) {
     const int sms = n_sm & ~1;
     const long long mean = ceil_div(rows, groups < rows ? groups : rows);  // rows of a group that has some
-    const long long blocks = dir == RAG_TN ? ceil_div(mean, 64) : ceil_div(k, i8 ? 128 : 64);
+    const int blocks = (int)(dir == RAG_TN ? ceil_div(mean, 64) : ceil_div(k, i8 ? 128 : 64));
+    auto columns = [&](int bn) { return dir == RAG_TN ? groups * ceil_div(k, bn) : chunks_of(groups, rows, bn); };
     ProductPlan best = {};
-    long long best_cost = -1;
-    auto offer = [&](bool pair, int bn, int split, long long tiles, long long at_once, long long extra) {
-        const long long cost =
-            ceil_div(tiles, at_once) * (ceil_div(blocks, split) * ((128 + (pair ? bn / 2 : bn)) * 128 / 45) + kTileClocks + extra);
-        if (best_cost >= 0 && cost >= best_cost) return;
+    double best_cost = 0.0;
+    auto offer = [&](bool pair, int bn, int split, long long tiles, int at_once, int once, int each) {
+        const double rounds = (double)((tiles + at_once - 1) / at_once);
+        const double cost = once + rounds * ((blocks + split - 1) / split * ((128 + (pair ? bn / 2 : bn)) * 128 / 45) + each);
+        if (best_cost > 0.0 && cost >= best_cost) return;
         best_cost = cost;
         best.pair = pair;
         best.bn = bn;
@@ -98,17 +100,18 @@ ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, i
         best.tiles = tiles;
         best.grid = (int)(2 * tiles < sms ? 2 * tiles : sms);
     };
-    auto columns = [&](int bn) { return dir == RAG_TN ? groups * ceil_div(k, bn) : chunks_of(groups, rows, bn); };
     for (int bn = 256; bn >= 128; bn /= 2) {
-        offer(true, bn, 1, columns(bn) * ceil_div(n, 256), sms / 2, 0);
-        if (2 * best.tiles >= 4 * sms) return best;  // rounds enough for their rest not to matter
+        const long long tiles = columns(bn) * ceil_div(n, 256);
+        offer(true, bn, 1, tiles, sms / 2, kPairClocks, kPairTileClocks);
+        if (tiles >= 2 * sms) return best;  // rounds enough for the rest of the last not to matter
     }
     for (int bn = 128; bn >= (dir == RAG_TN ? 64 : 16); bn /= 2) {
         const long long tiles = columns(bn) * ceil_div(n, 128);
         // parts of four blocks at least: a shorter one is over before its pipeline is full
         for (int split = 1; split <= SPLIT_MAX_CLUSTER && (split == 1 || 4 * split <= blocks); ++split) {
             const int at_once = split_clusters(split);
-            if (at_once > 0) offer(false, bn, split, tiles, at_once, split > 1 ? kMeetClocks : 0);
+            if (split > 1 && tiles > at_once) break;
+            if (at_once > 0) offer(false, bn, split, tiles, at_once, split > 1 ? kMeetClocks : 0, kSplitTileClocks);
         }
     }
     return best;

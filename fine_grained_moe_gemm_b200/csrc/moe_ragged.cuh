@@ -484,12 +484,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
 
-    if (threadIdx.x == 0) {
-        for (int b = 0; b < C::BARS; ++b) mbar_init(&bars[b], 1);
+    if (threadIdx.x < C::BARS) {
         // the two accumulators are released by every epilogue warp of both CTAs
-        for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], 2 * RAG_EPI_WARPS);
-        *abort_flag = 0;
+        const bool is_tempty = &bars[threadIdx.x] == tempty || &bars[threadIdx.x] == tempty + 1;
+        mbar_init(&bars[threadIdx.x], is_tempty ? 2 * RAG_EPI_WARPS : 1);
         fence_mbar_init();
+    } else if (threadIdx.x == RAG_THREADS - 1) {
+        *abort_flag = 0;
+        tma_prefetch_desc(&P.a);
+        tma_prefetch_desc(&P.b64);
+        if (DIR != RAG_TN) {
+            tma_prefetch_desc(&P.b128);
+            tma_prefetch_desc(&P.b16);
+        }
     }
     if (warp == 4) tmem_alloc_pair(tmem_slot);
     rag_build_table<RAG_THREADS>(P, tab, warp_sums, [&](int rows) { return rag_items_of<DIR>(P, rows); });

@@ -22,7 +22,7 @@ constexpr int SPLIT_EPI_WARPS = 8;
 constexpr int SPLIT_THREADS = (SPLIT_EPI_WARP0 + SPLIT_EPI_WARPS) * 32;
 constexpr int SPLIT_MAX_STAGES = 12;
 constexpr int SPLIT_TMEM_COLS = 256;  // two accumulators of 128 columns
-constexpr int SPLIT_BARS = 4 * SPLIT_MAX_STAGES + 5;
+constexpr int SPLIT_BARS = 3 * SPLIT_MAX_STAGES + 5;
 constexpr int SPLIT_MISC = (SPLIT_BARS * 8 + (2 + SPLIT_THREADS / 32) * 4 + 15) / 16 * 16;
 constexpr int SPLIT_TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;
 
@@ -113,11 +113,14 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     const int lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
 
-    if (threadIdx.x == 0) {
-        for (int b = 0; b < SPLIT_BARS; ++b) mbar_init(&bars[b], 1);
-        for (int b = 0; b < 2; ++b) mbar_init(&tempty[b], SPLIT_EPI_WARPS);
-        *abort_flag = 0;
+    if (threadIdx.x < SPLIT_BARS) {
+        const uint64_t* b = &bars[threadIdx.x];
+        mbar_init(&bars[threadIdx.x], b == tempty || b == tempty + 1 ? SPLIT_EPI_WARPS : 1);
         fence_mbar_init();
+    } else if (threadIdx.x == SPLIT_THREADS - 1) {
+        *abort_flag = 0;
+        tma_prefetch_desc(&P.a);
+        tma_prefetch_desc(&P.b64);
     }
     if (warp == 2) tmem_alloc<SPLIT_TMEM_COLS>(tmem_slot);
     const int mt = (P.n + 127) >> 7;
@@ -317,13 +320,13 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
         }
     }
 
-    // Every part is in its CTA's shared memory (a CTA that gave up has set the error word;
-    // its cluster stores what is there).
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();
-    const bool nothing = all_blocks == 0 && P.accumulate;  // a group without rows adds nothing
-    if (warp >= SPLIT_EPI_WARP0 && work && !nothing && !*abort_flag) {
+    // All parts are in their CTAs' shared memory.  (A CTA that gave up has set the error word; its
+    // peers go on with what is there.)
+    const bool stores = warp >= SPLIT_EPI_WARP0 && work && !(all_blocks == 0 && P.accumulate);
+    __syncwarp();
+    if (P.split > 1) cluster_sync_all();
+    else if (stores) named_bar_sync(1, SPLIT_EPI_WARPS * 32);
+    if (stores && !*abort_flag) {
         const uint32_t part = smem_u32(ring);
         const int t = threadIdx.x - SPLIT_EPI_WARP0 * 32;
         const int n_rows = DIR == RAG_TN ? min(128, P.n - f0) : width;      // rows of the output's tile
@@ -368,8 +371,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
             }
         }
     }
+    __syncwarp();
+    if (P.split > 1) cluster_sync_all();  // no CTA leaves while another reads its part
     tc_fence_before();
-    cluster_sync_all();  // no CTA leaves while another reads its part
+    __syncthreads();
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc<SPLIT_TMEM_COLS>(tmem_base);
