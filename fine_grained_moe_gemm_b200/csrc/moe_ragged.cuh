@@ -746,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
             if (!wait_acc()) break;
             const uint32_t t0 = lanes + (uint32_t)(buf * 256);
             if (DIR == RAG_TN) {
-                for (int c0 = 64 * half; c0 < it.width; c0 += 128) {
+                for (int c0 = 64 * half; c0 < it.width && f0 < P.n; c0 += 128) {
                     float v[32];
                     const bool wide = P.out != MOE_F32 && !P.accumulate;
 #pragma unroll
@@ -770,7 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(RAG_THREADS, 1)
                     if (wide) rag_store_h16_tile(P, stage, base, f0, it.col0 + c0);
                 }
             } else {
-                for (int c0 = 32 * half; c0 < it.width; c0 += 64) {
+                for (int c0 = 32 * half; c0 < it.width && f0 < P.n; c0 += 64) {
                     float v[32];
                     float sx = 0.0f;
                     if (I8 && c0 + lane < it.width) sx = __ldg(P.sx + it.row0 + c0 + lane);

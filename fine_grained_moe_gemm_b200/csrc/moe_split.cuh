@@ -15,9 +15,9 @@
 
 namespace moe {
 
-// Warps: 0 and 1 load A and B, 2 issues the MMAs, 3 zeroes TN's tail rows, 4-11 are the
-// epilogue.
-constexpr int SPLIT_EPI_WARP0 = 4;
+// Warps: 0-3 load, 4 issues the MMAs, 5 zeroes TN's tail rows, 8-15 are the epilogue, as in
+// moe_ragged.cuh.
+constexpr int SPLIT_EPI_WARP0 = 8;
 constexpr int SPLIT_EPI_WARPS = 8;
 constexpr int SPLIT_THREADS = (SPLIT_EPI_WARP0 + SPLIT_EPI_WARPS) * 32;
 constexpr int SPLIT_MAX_STAGES = 12;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
         tma_prefetch_desc(&P.a);
         tma_prefetch_desc(&P.b64);
     }
-    if (warp == 2) tmem_alloc<SPLIT_TMEM_COLS>(tmem_slot);
+    if (warp == 4) tmem_alloc<SPLIT_TMEM_COLS>(tmem_slot);
     const int mt = (P.n + 127) >> 7;
     rag_build_table<SPLIT_THREADS>(P, tab, warp_sums, [&](int rows) {
         return mt * (DIR == RAG_TN ? (P.k + bn - 1) / bn : (rows + bn - 1) / bn);
@@ -170,40 +170,38 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     const int q = warp & 3, half = (warp - SPLIT_EPI_WARP0) >> 2;
     bool ok = true;
 
-    if (warp < 2) {
-        if (elect_one()) {
-            const uint64_t policy = warp == 0 && DIR != RAG_TN ? l2_policy_evict_first() : l2_policy_evict_normal();
-            const int b_blocks = mma_n > 64 ? 2 : 1;  // TN: 64-column blocks
-            const uint32_t bytes = RAG_SLOT + (DIR == RAG_TN ? (uint32_t)(b_blocks * RAG_TN_BLOCK) : (uint32_t)bn * 128u);
+    if (warp < 4) {
+        const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT) || (warp == 3 && DIR == RAG_TN);
+        if (works && elect_one()) {
+            const bool is_a = warp < 2;
+            const int half = (warp & 1) * 64;
+            // weights that one chunk reads stream; those of several chunks stay for the others
+            const uint64_t policy = DIR == RAG_TN || !is_a ? l2_policy_evict_normal()
+                                    : tab.count[g] > bn   ? l2_policy_evict_last() : l2_policy_evict_first();
+            const bool second = mma_n > 64;  // TN: B has a second 64-column block
+            const uint32_t bytes = RAG_SLOT + (DIR == RAG_TN ? (second ? 2u : 1u) * RAG_TN_BLOCK : (uint32_t)bn * 128u);
             int slot = 0;
             uint32_t phase = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait_bounded(&empty[slot], phase ^ 1u, abort_flag)) break;
-                uint8_t* sa = ring + slot * stage_bytes;
-                uint8_t* sb = sa + RAG_SLOT;
+                uint8_t* dst = ring + slot * stage_bytes + (is_a ? 0 : RAG_SLOT) + half * 128;
                 const bool tail = DIR == RAG_TN && kb == all_blocks - 1 && (rows & 15);
                 uint64_t* bar = tail ? &landed[slot] : &full[slot];
-                if (warp == 0) {
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (DIR == RAG_NT) {
-                        tma_load_3d(sa, &P.a, kb * block_k, f0, g, bar, policy);
-                    } else if (DIR == RAG_NN) {
-                        tma_load_3d(sa, &P.a, f0, kb * 64, g, bar, policy);
-                        tma_load_3d(sa + RAG_TN_BLOCK, &P.a, f0 + 64, kb * 64, g, bar, policy);
-                    } else {
-                        tma_load_2d(sa, &P.a, f0, row0 + kb * 64, bar, policy);
-                        tma_load_2d(sa + RAG_TN_BLOCK, &P.a, f0 + 64, row0 + kb * 64, bar, policy);
-                    }
-                } else if (DIR == RAG_TN) {
-                    tma_load_2d(sb, &P.b64, col0, row0 + kb * 64, bar, policy);
-                    if (b_blocks == 2) tma_load_2d(sb + RAG_TN_BLOCK, &P.b64, col0 + 64, row0 + kb * 64, bar, policy);
+                if (warp == 0) mbar_arrive_expect_tx(bar, bytes);
+                if (DIR == RAG_TN) {
+                    if (is_a) tma_load_2d(dst, &P.a, f0 + half, row0 + kb * 64, bar, policy);
+                    else if (half == 0 || second) tma_load_2d(dst, &P.b64, col0 + half, row0 + kb * 64, bar, policy);
+                } else if (!is_a) {
+                    tma_load_2d(dst, &P.b64, kb * block_k, row0, bar, policy);
+                } else if (DIR == RAG_NT) {
+                    tma_load_3d(dst, &P.a, kb * block_k, f0, g, bar, policy);
                 } else {
-                    tma_load_2d(sb, &P.b64, kb * block_k, row0, bar, policy);
+                    tma_load_3d(dst, &P.a, f0 + half, kb * 64, g, bar, policy);
                 }
                 if (++slot == stages) { slot = 0; phase ^= 1u; }
             }
         }
-    } else if (warp == 2) {
+    } else if (warp == 4) {
         if (elect_one()) {
             constexpr uint64_t a_step = DIR == RAG_NT ? 2 : 128, b_step = DIR == RAG_TN ? 128 : 2;
             constexpr int per_step = I8 ? 32 : 16;
@@ -225,10 +223,19 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
                     tc_fence_after();
                     const uint64_t ad = ad0 + stage_step * slot, bd = bd0 + stage_step * slot;
                     const int steps = min(4, (len - kb * block_k + per_step - 1) / per_step);
-                    for (int s = 0; s < steps; ++s) {
-                        const uint32_t accum = (kb > s0 || s != 0) ? 1u : 0u;
-                        if (I8) mma_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
-                        else mma_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                    if (steps == 4) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            const uint32_t accum = (kb > s0 || s != 0) ? 1u : 0u;
+                            if (I8) mma_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                            else mma_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                        }
+                    } else {
+                        for (int s = 0; s < steps; ++s) {
+                            const uint32_t accum = (kb > s0 || s != 0) ? 1u : 0u;
+                            if (I8) mma_i8(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                            else mma_bf16(d, ad + a_step * s, bd + b_step * s, idesc, accum);
+                        }
                     }
                     mma_commit(&empty[slot]);
                     issued = true;
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
                 mbar_wait_bounded(drain, 0, &dummy, 100000000ull);
             }
         }
-    } else if (warp == 3) {
+    } else if (warp == 5) {
         if (DIR == RAG_TN && kb1 == all_blocks && kb1 > kb0 && (rows & 15)) {
             // this CTA has the group's last rows: zeros behind them (see moe_ragged.cuh)
             const int slot = (kb1 - 1 - kb0) % stages;
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
                 if (lane == 0) mbar_arrive(&full[slot]);
             }
         }
-    } else {
+    } else if (warp >= SPLIT_EPI_WARP0) {
         // ------------------------------------------------------------ the part's sums
         int buf = 0;
         uint32_t acc_phase = 0;
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     if (P.split > 1) cluster_sync_all();  // no CTA leaves while another reads its part
     tc_fence_before();
     __syncthreads();
-    if (warp == 2) {
+    if (warp == 4) {
         tc_fence_after();
         tmem_dealloc<SPLIT_TMEM_COLS>(tmem_base);
     }
