@@ -180,6 +180,7 @@ struct RaggedArgs {
     const float* sx;       // 8-bit operands: scale of each row, and of each [group][n]
     const float* sw;
     int bn;      // columns of a tile: 256 or 128; moe_split_kernel: 128, 64, 32 or 16 (TN: 128 or 64)
+    int bn_shift;  // log2 of bn
     // moe_split_kernel (b64 is then its only map of the rows, in boxes of bn rows; TN 64 x 64)
     int split;   // CTAs that share a tile's summed axis
     int stages;  // of the ring

@@ -119,6 +119,7 @@ ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, i
 
 moe_status run_product(int dir, bool i8, RaggedArgs* a, const ProductPlan& p, cudaStream_t s) {
     a->bn = p.bn;
+    while ((1 << a->bn_shift) < p.bn) ++a->bn_shift;
     a->split = p.split;
     return cuda_status(p.pair ? launch_ragged(dir, i8, a, p.grid, s) : launch_split(dir, i8, a, p.tiles, s));
 }

@@ -86,7 +86,7 @@ struct RagTable {
 // Chunks of a group of `rows` rows (TN: column tiles of its dw), and its items.
 template <int DIR>
 __device__ __forceinline__ int rag_chunks(const RaggedArgs& P, int rows) {
-    return ((DIR == RAG_TN ? P.k : rows) + P.bn - 1) / P.bn;
+    return ((DIR == RAG_TN ? P.k : rows) + P.bn - 1) >> P.bn_shift;
 }
 template <int DIR>
 __device__ __forceinline__ int rag_items_of(const RaggedArgs& P, int rows) {
@@ -156,17 +156,20 @@ __device__ __forceinline__ RagItem rag_item(const RaggedArgs& P, const RagTable&
     const int mt = (P.n + 255) >> 8;
     const int nc = rag_chunks<DIR>(P, it.rows);
     int local = i - t.first[lo];
-    const int band = local / (RAG_BAND * mt);
-    local -= band * RAG_BAND * mt;
+    int band = 0;
+    if (local >= RAG_BAND * mt) {
+        band = local / (RAG_BAND * mt);
+        local -= band * RAG_BAND * mt;
+    }
     const int nb = min(RAG_BAND, nc - band * RAG_BAND);
-    it.m = local / nb;
+    it.m = nb == 1 ? local : nb == RAG_BAND ? local / RAG_BAND : local / nb;
     const int c = band * RAG_BAND + local - it.m * nb;
     it.chunks = nc;
     if (DIR == RAG_TN) {
         it.col0 = c * P.bn;
         it.width = min(P.bn, P.k - it.col0);
     } else {
-        const int w = ((it.rows + nc - 1) / nc + 31) & ~31;  // equal chunks, at most bn rows
+        const int w = nc == 1 ? P.bn : ((it.rows + nc - 1) / nc + 31) & ~31;  // equal chunks, at most bn rows
         it.col0 = 0;
         it.row0 += c * w;
         it.width = min(w, it.rows - c * w);
@@ -263,15 +266,18 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_
 }
 
 // fp32 -> 16-bit bits, one rounding to nearest even.
-__device__ __forceinline__ uint32_t rag_pack2(float a, float b, int bf16) {
-    if (bf16) {
+template <bool BF16>
+__device__ __forceinline__ uint32_t rag_pack2(float a, float b) {
+    if (BF16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint16_t rag_pack1(float a, int bf16) { return (uint16_t)(rag_pack2(a, a, bf16) & 0xffffu); }
+__device__ __forceinline__ uint32_t rag_pack2(float a, float b, int bf16) {
+    return bf16 ? rag_pack2<true>(a, b) : rag_pack2<false>(a, b);
+}
 __device__ __forceinline__ float rag_unpack(uint16_t v, int bf16) {
     if (bf16) return __uint_as_float((uint32_t)v << 16);
     return __half2float(__ushort_as_half(v));
@@ -308,41 +314,62 @@ __device__ __forceinline__ void rag_store_rows_f32(const RaggedArgs& P, uint8_t*
     }
 }
 
+// 16-bit results.  A word of the stage holds two rows' values of one feature (one
+// conversion and one store for two values); a lane takes eight features of a pair of rows
+// back and parts them.  Reading the two 16-byte halves in the other order on odd pairs
+// keeps a quarter warp on different banks.
+template <bool BF16>
+__device__ __forceinline__ void rag_store_rows_h16(const RaggedArgs& P, uint8_t* stage, int row0, int valid, int f0,
+                                                   const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    uint32_t* st = reinterpret_cast<uint32_t*>(stage);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) st[j * 32 + lane] = rag_pack2<BF16>(v[2 * j], v[2 * j + 1]);
+    __syncwarp();
+    const int part = lane & 3, odd = (lane >> 2) & 1;
+    if (f0 + part * 8 < P.n) {
+        uint16_t* y = static_cast<uint16_t*>(P.y) + (size_t)(row0 + 2 * (lane >> 2)) * P.ldy + f0 + part * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = 16 * i + 2 * (lane >> 2);  // the pair's first row
+            const uint4* src = reinterpret_cast<const uint4*>(st + (j >> 1) * 32 + part * 8);
+            const uint4 p = src[odd], q = src[odd ^ 1];
+            const uint4 lo = odd ? q : p, hi = odd ? p : q;
+            if (j < valid)
+                *reinterpret_cast<uint4*>(y + (size_t)(16 * i) * P.ldy) =
+                    make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                               __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
+            if (j + 1 < valid)
+                *reinterpret_cast<uint4*>(y + (size_t)(16 * i + 1) * P.ldy) =
+                    make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                               __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
+        }
+    }
+    __syncwarp();
+}
+
 __device__ __forceinline__ void rag_store_rows(const RaggedArgs& P, uint8_t* stage, int row0, int valid, int f0,
                                                const float (&v)[32]) {
     const int lane = threadIdx.x & 31;
-    const int bf16 = P.out == MOE_BF16;
     if (P.out == MOE_F32) {
         rag_store_rows_f32(P, stage, row0, valid, f0, v);
-        return;
-    }
-    if (P.accumulate) {  // added in fp32 and rounded once: in place, two bytes a lane
+    } else if (P.accumulate) {  // added in fp32 and rounded once: in place, two bytes a lane
+        const int bf16 = P.out == MOE_BF16;
         if (f0 + lane < P.n) {
             uint16_t* y = static_cast<uint16_t*>(P.y) + (size_t)row0 * P.ldy + f0 + lane;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
                 if (j < valid) {
                     uint16_t* p = y + (size_t)j * P.ldy;
-                    *p = rag_pack1(rag_unpack(*p, bf16) + v[j], bf16);
+                    const float s = rag_unpack(*p, bf16) + v[j];
+                    *p = (uint16_t)(rag_pack2(s, s, bf16) & 0xffffu);
                 }
         }
-        return;
+    } else if (P.out == MOE_BF16) {
+        rag_store_rows_h16<true>(P, stage, row0, valid, f0, v);
+    } else {
+        rag_store_rows_h16<false>(P, stage, row0, valid, f0, v);
     }
-    uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) st[j * 32 + lane] = rag_pack1(v[j], bf16);
-    __syncwarp();
-    const int part = lane & 3;
-    if (f0 + part * 8 < P.n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = i * 8 + (lane >> 2);
-            if (j < valid)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.y) + (size_t)(row0 + j) * P.ldy + f0 + part * 8) =
-                    *reinterpret_cast<const uint4*>(stage + j * 64 + part * 16);
-        }
-    }
-    __syncwarp();
 }
 
 // Epilogue of TN: lane holds row f0 + lane of dw, columns c0 .. (32 fp32 values, or 64
