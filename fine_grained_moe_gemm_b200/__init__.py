@@ -784,8 +784,8 @@ def moe_swiglu(gate, up, h, coef=None, n_rows=None, stream=None):
 
 
 def moe_swiglu_backward(dh, gate, up, dgate, dup, coef=None, dcoef=None, n_rows=None, stream=None):
-    """The gradients of ``moe_swiglu``: dgate, dup (like gate), and dcoef fp32 [R] when given.  dgate may be gate,
-    dup may be up or dh."""
+    """The gradients of ``moe_swiglu``: dgate, dup (like gate), and dcoef fp32 [R] when given.  dgate and
+    dup may each be one of dh, gate and up itself."""
     dev, shape, t = _home(gate, "gate"), gate.shape, (gate.dtype,)
     pg, ldg = _rows(gate, "gate", dev, shape, _FLOATS)
     pd, ldd = _rows(dh, "dh", dev, shape, t)

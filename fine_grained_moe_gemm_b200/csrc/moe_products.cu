@@ -28,6 +28,27 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // distance of rows: holds a row and keeps every row on a 16-byte boundary
 bool good_ld(int64_t ld, int width, int elem) { return ld >= width && ld <= kMaxLd && (ld * elem) % 16 == 0; }
 
+// Whether two matrices of `rows` rows share bytes (p: address, ld: bytes from row to row, w:
+// bytes of a row).  Columns of one wider buffer do not; different row distances over a
+// common range count as sharing.
+struct Rows {
+    const void* p;
+    int64_t ld, w;
+};
+bool share(const Rows& a, const Rows& b, int rows) {
+    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a.p), pb = (int64_t)reinterpret_cast<uintptr_t>(b.p);
+    const int64_t ea = pa + (rows - 1) * a.ld + a.w, eb = pb + (rows - 1) * b.ld + b.w;
+    if (ea <= pb || eb <= pa) return false;
+    if (a.ld != b.ld) return true;
+    const int64_t d = ((pb - pa) % a.ld + a.ld) % a.ld;  // b's columns start d bytes behind a's
+    return d < a.w || a.ld - d < b.w;
+}
+bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld; }
+// one block of bytes against rows
+bool share(const void* p, size_t bytes, const Rows& r, int rows) {
+    return share(Rows{p, (int64_t)bytes, (int64_t)bytes}, Rows{r.p, (rows - 1) * r.ld + r.w, (rows - 1) * r.ld + r.w}, 1);
+}
+
 // Shapes and flags that every product checks; k_step: elements of 16 bytes of the operands.
 moe_status check_product(int groups, int rows, int n, int k, int k_step, const int32_t* offsets, moe_dtype out,
                          moe_dtype operands, int accumulate) {
@@ -175,6 +196,8 @@ moe_status moe_grouped_mm(int groups, int rows, int n, int k, moe_dtype dtype, c
     if (rows == 0) return MOE_OK;
     if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
     if (!good_ld(ldx, k, 2) || !good_ld(ldy, n, size_of(y_dtype))) return MOE_ERR_INVALID_ARG;
+    const Rows rx = {x, ldx * 2, k * 2}, ry = {y, ldy * size_of(y_dtype), n * size_of(y_dtype)};
+    if (share(rx, ry, rows) || share(w, (size_t)groups * n * k * 2, ry, rows)) return MOE_ERR_INVALID_ARG;
     return product(false, dtype, groups, rows, n, k, x, ldx, w, transpose_w, nullptr, nullptr, offsets, y, ldy,
                    y_dtype, accumulate, stream);
 }
@@ -189,6 +212,8 @@ moe_status moe_grouped_mm_int8(int groups, int rows, int n, int k, const int8_t*
     if (!q || !w || !y || !sx || !sw || !aligned16(q) || !aligned16(w) || !aligned16(y) || !aligned4(sx) ||
         !aligned4(sw) || !good_ld(ldy, n, size_of(y_dtype)))
         return MOE_ERR_INVALID_ARG;
+    const Rows rq = {q, k, k}, ry = {y, ldy * size_of(y_dtype), n * size_of(y_dtype)};
+    if (share(rq, ry, rows) || share(w, (size_t)groups * n * k, ry, rows)) return MOE_ERR_INVALID_ARG;
     return product(true, y_dtype, groups, rows, n, k, q, k, w, 0, sx, sw, offsets, y, ldy, y_dtype, accumulate, stream);
 }
 
@@ -202,11 +227,14 @@ moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dtype dtype
     if (!dw || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
     if (rows && (!dy || !x || !aligned16(dy) || !aligned16(x) || !good_ld(lddy, n, 2) || !good_ld(ldx, k, 2)))
         return MOE_ERR_INVALID_ARG;
+    const size_t dw_bytes = (size_t)groups * n * k * size_of(dw_dtype);
+    if (rows && (share(dw, dw_bytes, Rows{dy, lddy * 2, n * 2}, rows) || share(dw, dw_bytes, Rows{x, ldx * 2, k * 2}, rows)))
+        return MOE_ERR_INVALID_ARG;
     DevInfo di;
     if ((st = check_device(&di)) != MOE_OK) return st;
     if (rows == 0) {  // a sum of nothing
         if (accumulate) return MOE_OK;
-        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)groups * n * k * size_of(dw_dtype), (cudaStream_t)stream));
+        return cuda_status(cudaMemsetAsync(dw, 0, dw_bytes, (cudaStream_t)stream));
     }
     RaggedArgs a;
     memset(&a, 0, sizeof(a));
@@ -237,6 +265,9 @@ moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* gate, in
     if (!gate || !up || !h || !aligned16(gate) || !aligned16(up) || !aligned16(h) || !aligned4(coef) ||
         !aligned4(n_rows) || !good_ld(ld_gate, width, e) || !good_ld(ld_up, width, e) || !good_ld(ld_h, width, e))
         return MOE_ERR_INVALID_ARG;
+    const int64_t wide = (int64_t)width * e;
+    const Rows rg = {gate, ld_gate * e, wide}, ru = {up, ld_up * e, wide}, rh = {h, ld_h * e, wide};
+    if ((share(rg, rh, rows) && !same(rg, rh)) || (share(ru, rh, rows) && !same(ru, rh))) return MOE_ERR_INVALID_ARG;
     DevInfo di;
     const moe_status st = check_device(&di);
     if (st != MOE_OK) return st;
@@ -269,6 +300,13 @@ moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, const void*
         !good_ld(ld_dh, width, e) || !good_ld(ld_gate, width, e) || !good_ld(ld_up, width, e) ||
         !good_ld(ld_dgate, width, e) || !good_ld(ld_dup, width, e))
         return MOE_ERR_INVALID_ARG;
+    const int64_t wide = (int64_t)width * e;
+    const Rows in[3] = {{dh, ld_dh * e, wide}, {gate, ld_gate * e, wide}, {up, ld_up * e, wide}};
+    const Rows out[2] = {{dgate, ld_dgate * e, wide}, {dup, ld_dup * e, wide}};
+    if (share(out[0], out[1], rows)) return MOE_ERR_INVALID_ARG;
+    for (const Rows& i : in)
+        for (const Rows& o : out)
+            if (share(i, o, rows) && !same(i, o)) return MOE_ERR_INVALID_ARG;
     DevInfo di;
     const moe_status st = check_device(&di);
     if (st != MOE_OK) return st;
@@ -300,6 +338,8 @@ moe_status moe_quantize_int8(const void* x, moe_dtype dtype, int64_t ldx, int ro
     if (rows == 0) return MOE_OK;
     if (!x || !q || !sx || !aligned16(x) || !aligned16(q) || !aligned4(sx) || !aligned4(n_rows) ||
         !good_ld(ldx, k, size_of(dtype)))
+        return MOE_ERR_INVALID_ARG;
+    if (share(q, (size_t)rows * k, Rows{x, ldx * size_of(dtype), (int64_t)k * size_of(dtype)}, rows))
         return MOE_ERR_INVALID_ARG;
     DevInfo di;
     const moe_status st = check_device(&di);

@@ -342,7 +342,8 @@ MOE_API moe_status moe_dense_ffn(int d, int hidden, moe_dtype act_dtype, moe_dty
  *   - ld*: elements from one row to the next, at least the row, a multiple of 16
  *     bytes; so halves of a wider buffer can be read and written in place.  Weights
  *     and their gradients are dense.
- *   - Outputs may not overlap inputs.  One launch, no workspace, results that do
+ *   - Outputs may not share bytes with inputs (MOE_ERR_INVALID_ARG; disjoint columns of
+ *     one buffer are fine).  One launch, no workspace, results that do
  *     not depend on the run; sums in fp32 (8-bit operands: exact in 32 bits),
  *     rounded once.  accumulate = 1 adds to the output, before that rounding. */
 
@@ -371,7 +372,8 @@ MOE_API moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dty
  * multiple of 8, at most 65536; coef [rows] fp32, or NULL for 1; n_rows: device count
  * of the rows to compute (e.g. offsets + groups; the rows behind are left as they
  * were; a count outside [0, rows] computes none and sets MOE_DEVERR_BAD_ROWS), or
- * NULL for all.  Computed in fp32, rounded once.  h may be gate or up itself. */
+ * NULL for all.  Computed in fp32, rounded once.  h may be gate or up itself, else shares no
+ * bytes with them. */
 MOE_API moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* gate, int64_t ld_gate, const void* up,
                               int64_t ld_up, const float* coef, const int32_t* n_rows, void* h, int64_t ld_h,
                               moe_stream_t stream);
@@ -379,7 +381,8 @@ MOE_API moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* 
 /* The gradients of moe_swiglu from dh: with s = sigmoid(gate), a = gate * s
  *   dgate = coef * dh * up * (s + a * (1 - s)),  dup = coef * dh * a,
  *   dcoef[r] = sum over the row of dh * a * up     fp32 [rows], or NULL
- * dgate may be gate and dup may be up (or dh) itself.  The sum has a fixed order. */
+ * dgate and dup may each be one of dh, gate and up itself, not the same one; else they
+ * share no bytes with them.  The sum has a fixed order. */
 MOE_API moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, const void* dh, int64_t ld_dh,
                                        const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
                                        const float* coef, const int32_t* n_rows, void* dgate, int64_t ld_dgate,

@@ -579,3 +579,158 @@ def test_int8_ffn_against_the_bf16_one():
     err = (got - t["y"].double()).square().mean().sqrt()
     assert float(err) <= 0.05 * float(t["y"].double().square().mean().sqrt())
     assert moe.device_error() == 0
+
+
+def test_layer_from_the_operators_matches_the_layer():
+    """moe_permute's offsets and rows through the grouped products give the routed part of moe_forward.  Where the two
+    round to bf16 differs: gate and up here, and h in both (once with its coefficient, once without): four roundings
+    of relative error at most u = 2^-8, u / sqrt(3) as a root mean square, independent from element to element.  Each
+    enters y linearly (gate's through SiLU, whose relative slope is about 1), so the root mean square of the
+    difference is about 2 u / sqrt(3) of y's; 2 u leaves room for the slopes above 1.  The largest of the 150,000
+    elements lies some five times further out, so it is not what is tested."""
+    from moe_testlib import cfg_of
+    from workloads import WORKLOADS, make_inputs
+    import dataclasses
+    wl = dataclasses.replace(WORKLOADS["tiny"], T=300, x_f32=False, d=512, hidden=256)
+    W = {k: v.to(DEV) for k, v in make_inputs(wl, "cpu").items()}
+    cfg = cfg_of(wl)
+    cfg.n_shared, cfg.shared_hidden = 0, 0
+    T, k, E, R = wl.T, wl.top_k, wl.n_experts, wl.T * wl.top_k
+    x = W["x"]
+    ws = torch.empty(moe.workspace_size(cfg, T), dtype=torch.uint8, device=DEV)
+    y = torch.empty((T, wl.d), device=DEV)
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=DEV)
+    out = {"topk_idx": i32(T, k), "topk_w": torch.empty((T, k), device=DEV), "offsets": i32(E + 1), "src": i32(R)}
+    moe.moe_forward(cfg, {n: W[n] for n in ("w_router", "w_gate", "w_up", "w_down")}, x, W["bias"], y, workspace=ws,
+                    routing_out=out)
+    src = out["src"].long()
+    rows = x[src // k].contiguous()
+    coef = (out["topk_w"].view(-1)[src] * wl.routed_scale).contiguous()
+    gu = torch.empty((R, 2 * wl.hidden), dtype=BF, device=DEV)
+    gate, up = gu[:, :wl.hidden], gu[:, wl.hidden:]
+    o = torch.empty((R, wl.d), device=DEV)
+    off = out["offsets"]
+    moe.moe_grouped_mm(rows, W["w_gate"], off, gate)
+    moe.moe_grouped_mm(rows, W["w_up"], off, up)
+    moe.moe_swiglu(gate, up, gate, coef=coef, n_rows=off[-1:])
+    moe.moe_grouped_mm(gate, W["w_down"], off, o)
+    got = torch.zeros_like(y).index_add_(0, src // k, o)
+    assert moe.device_error() == 0
+    assert float((got - y).square().mean().sqrt()) <= 2 * 2.0 ** -8 * float(y.square().mean().sqrt())
+
+
+def test_outputs_past_two_to_the_31_elements():
+    gen = _gen(41)
+    rows, n, k = 280_000, 8192, 64                      # y: 2.3e9 elements
+    x, w = _rand(gen, (rows, k), BF), _rand(gen, (3, n, k), BF)
+    sizes = [100_000, 0, 180_000]
+    y = torch.zeros((rows, n), dtype=BF, device=DEV)
+    moe.moe_grouped_mm(x, w, _offsets(sizes), y)
+    for r in (0, 99_999, 100_000, 262_143, 262_144, rows - 1):
+        g = 0 if r < 100_000 else 2
+        ref, mag = x[r].double() @ w[g].double().t(), x[r].double().abs() @ w[g].double().abs().t()
+        _within(y[r], ref, 66 * 2.0 ** -23 * mag * 1.01 + _eps(BF) * ref.abs(), f"row {r}")
+    del y
+    dy = _rand(gen, (rows, 2048), BF)
+    sizes = [rows // 1000] * 1000 + [0] * 23 + [rows - rows // 1000 * 1000]
+    dw = torch.zeros((1024, 2048, 1088), dtype=BF, device=DEV)   # 2.3e9 elements
+    x = _rand(gen, (rows, 1088), BF)
+    moe.moe_grouped_wgrad(dy, x, _offsets(sizes), dw)
+    starts = np.concatenate([[0], np.cumsum(sizes)])
+    for g in (0, 500, 963, 964, 999, 1000, 1023):
+        a, b = dy[starts[g]:starts[g + 1]].double(), x[starts[g]:starts[g + 1]].double()
+        ref, mag = a.t() @ b, a.abs().t() @ b.abs()
+        _within(dw[g], ref, 290 * 2.0 ** -23 * mag * 1.01 + _eps(BF) * ref.abs(), f"group {g}")
+    assert moe.device_error() == 0
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: no call needs an eager one before it."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, fine_grained_moe_gemm_b200 as moe
+t = lambda *s, d=torch.bfloat16: torch.ones(s, dtype=d, device="cuda")
+x, w, wide = t(20, 64), t(2, 48, 64), t(2, 4096, 64)
+off = torch.tensor([0, 7, 20], dtype=torch.int32, device="cuda")
+big, xb = torch.tensor([0, 3000, 6000], dtype=torch.int32, device="cuda"), t(6000, 64)
+y, yb, dw, dwb = t(20, 48), t(6000, 4096), t(2, 48, 64, d=torch.float32), t(2, 4096, 64, d=torch.float32)
+q, sx = torch.zeros((20, 64), dtype=torch.int8, device="cuda"), t(20, d=torch.float32)
+wq, sw = torch.ones((2, 48, 64), dtype=torch.int8, device="cuda"), t(2, 48, d=torch.float32)
+h, dh = t(20, 48), t(20, 48)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    moe.moe_grouped_mm(x, w, off, y)
+    moe.moe_grouped_mm(xb, wide, big, yb)
+    moe.moe_grouped_wgrad(y, x, off, dw)
+    moe.moe_grouped_wgrad(yb, xb, big, dwb)
+    moe.moe_swiglu(y, y, h)
+    moe.moe_swiglu_backward(dh, y, y, h, dh)
+    moe.moe_quantize_int8(x, q, sx)
+    moe.moe_grouped_mm_int8(q, sx, wq, sw, off, y)
+g.replay()
+torch.cuda.synchronize()
+assert moe.device_error() == 0
+assert float(yb.float().min()) == float(yb.float().max()) == 64.0
+assert abs(float(y.float().max()) - 64.0) < 0.5 and float(dw[1].max()) == 13 * 64.0 and float(dwb.max()) == 3000 * 64.0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_many_calls_on_several_streams_at_once():
+    """Products of both tilings, gradients and codes interleaved on four streams give the results of calls alone."""
+    jobs = []
+    for i in range(4):
+        gen = _gen(60 + i)
+        sizes = [[5, 0, 900, 40], [1, 2, 3], [300] * 6, [0, 2000]][i]
+        n, k = [(1032, 520), (72, 2056), (2048, 256), (264, 1024)][i]
+        R = sum(sizes)
+        j = {"x": _rand(gen, (R, k), BF), "w": _rand(gen, (len(sizes), n, k), BF, 0.1), "dy": _rand(gen, (R, n), BF),
+             "off": _offsets(sizes), "y": torch.empty((R, n), device=DEV), "dx": torch.empty((R, k), dtype=BF, device=DEV),
+             "dw": torch.empty((len(sizes), n, k), device=DEV), "stream": torch.cuda.Stream()}
+        jobs.append(j)
+
+    def call(j, s):
+        moe.moe_grouped_mm(j["x"], j["w"], j["off"], j["y"], stream=s)
+        moe.moe_grouped_mm(j["dy"], j["w"], j["off"], j["dx"], transpose_w=True, stream=s)
+        moe.moe_grouped_wgrad(j["dy"], j["x"], j["off"], j["dw"], stream=s)
+
+    want = []
+    for j in jobs:
+        call(j, None)
+        torch.cuda.synchronize()
+        want.append([j[n].clone() for n in ("y", "dx", "dw")])
+        for n in ("y", "dx", "dw"):
+            j[n].fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            call(j, j["stream"])
+    torch.cuda.synchronize()
+    for j, w in zip(jobs, want):
+        for n, r in zip(("y", "dx", "dw"), w):
+            assert torch.equal(j[n], r), n
+    assert moe.device_error() == 0
+
+
+def test_binding_refusals_on_the_gpu():
+    x, w = torch.zeros((4, 16), dtype=BF, device=DEV), torch.zeros((2, 8, 16), dtype=BF, device=DEV)
+    off, y = torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros((4, 8), dtype=BF, device=DEV)
+    ok = lambda **kw: moe.moe_grouped_mm(**{**dict(x=x, w=w, offsets=off, y=y), **kw})
+    ok()
+    for bad in (dict(x=x[:, :8]), dict(x=x.half()), dict(x=x.t()), dict(w=w[0]), dict(w=w.float()), dict(offsets=off.long()),
+                dict(offsets=off[:2]), dict(offsets=None), dict(y=y.half()), dict(y=y[:3]), dict(x=x.cpu()),
+                dict(w=w.transpose(1, 2)), dict(y=y[:, :1].expand(4, 8))):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(moe.MoeError):      # rows that are not 16 bytes apart
+        ok(x=torch.zeros((4, 20), dtype=BF, device=DEV)[:, :16])
+    with pytest.raises(moe.MoeError):      # rows that lie on one another
+        ok(x=torch.zeros((1, 16), dtype=BF, device=DEV).expand(4, 16))
+    with pytest.raises(moe.MoeError):      # a sum of 12
+        ok(x=torch.zeros((4, 12), dtype=BF, device=DEV), w=torch.zeros((2, 8, 12), dtype=BF, device=DEV))
+    assert moe.device_error() == 0

@@ -13,7 +13,10 @@ B16, H16, F32, E43 = moe.MOE_BF16, moe.MOE_F16, moe.MOE_F32, moe.MOE_E4M3
 NO_GPU = not torch.cuda.is_available()
 
 
-def _mm(groups=4, rows=10, n=64, k=32, dtype=B16, x=16, ldx=32, w=16, tr=0, off=16, y=16, ldy=64, out=B16, acc=0):
+X, W, Y, Z, V = (i << 24 for i in range(1, 6))   # addresses far apart
+
+
+def _mm(groups=4, rows=10, n=64, k=32, dtype=B16, x=X, ldx=32, w=W, tr=0, off=16, y=Y, ldy=64, out=B16, acc=0):
     p = lambda v: None if v is None else P(v)
     return moe.lib().moe_grouped_mm(groups, rows, n, k, dtype, p(x), ldx, p(w), tr, p(off), p(y), ldy, out, acc, None)
 
@@ -38,7 +41,7 @@ def test_mm_types_and_nothing_to_do():
         assert _mm() == UNS and _mm(groups=1, off=None) == UNS
 
 
-def _wgrad(groups=4, rows=10, n=64, k=32, dtype=B16, dy=16, lddy=64, x=16, ldx=32, off=16, dw=16, out=F32, acc=0):
+def _wgrad(groups=4, rows=10, n=64, k=32, dtype=B16, dy=Y, lddy=64, x=X, ldx=32, off=16, dw=W, out=F32, acc=0):
     p = lambda v: None if v is None else P(v)
     return moe.lib().moe_grouped_wgrad(groups, rows, n, k, dtype, p(dy), lddy, p(x), ldx, p(off), p(dw), out, acc, None)
 
@@ -55,7 +58,7 @@ def test_wgrad_types():
         assert _wgrad() == UNS and _wgrad(rows=0, dy=None, x=None) == UNS
 
 
-def _mm8(groups=4, rows=10, n=64, k=32, q=16, sx=4, w=16, sw=4, off=16, y=16, ldy=64, out=B16, acc=0):
+def _mm8(groups=4, rows=10, n=64, k=32, q=X, sx=4, w=W, sw=4, off=16, y=Y, ldy=64, out=B16, acc=0):
     p = lambda v: None if v is None else P(v)
     return moe.lib().moe_grouped_mm_int8(groups, rows, n, k, p(q), p(sx), p(w), p(sw), p(off), p(y), ldy, out, acc, None)
 
@@ -74,12 +77,12 @@ def test_mm_int8_accepts():
             assert _mm8(out=out) == UNS
 
 
-def _swiglu(rows=4, width=64, dtype=B16, gate=16, ldg=64, up=16, ldu=64, coef=None, n=None, h=16, ldh=64):
+def _swiglu(rows=4, width=64, dtype=B16, gate=X, ldg=64, up=W, ldu=64, coef=None, n=None, h=Y, ldh=64):
     p = lambda v: None if v is None else P(v)
     return moe.lib().moe_swiglu(rows, width, dtype, p(gate), ldg, p(up), ldu, p(coef), p(n), p(h), ldh, None)
 
 
-def _swiglu_b(rows=4, width=64, dtype=B16, dh=16, gate=16, up=16, coef=None, n=None, dgate=16, dup=16, dcoef=None, ld=64):
+def _swiglu_b(rows=4, width=64, dtype=B16, dh=X, gate=W, up=Y, coef=None, n=None, dgate=Z, dup=V, dcoef=None, ld=64):
     p = lambda v: None if v is None else P(v)
     return moe.lib().moe_swiglu_backward(rows, width, dtype, p(dh), ld, p(gate), ld, p(up), ld, p(coef), p(n), p(dgate), ld,
                                          p(dup), ld, p(dcoef), None)
@@ -103,7 +106,7 @@ def test_swiglu_more():
         assert _swiglu() == UNS and _swiglu(dtype=F32) == UNS and _swiglu_b(coef=16, dcoef=16) == UNS
 
 
-def _quant(x=16, dtype=B16, ldx=64, rows=4, k=64, n=None, q=16, sx=16):
+def _quant(x=X, dtype=B16, ldx=64, rows=4, k=64, n=None, q=Y, sx=16):
     p = lambda v: None if v is None else P(v)
     return moe.lib().moe_quantize_int8(p(x), dtype, ldx, rows, k, p(n), p(q), p(sx), None)
 
@@ -118,6 +121,30 @@ def test_quantize_more():
     assert _quant(dtype=E43) == UNS and _quant(rows=0, x=None, q=None, sx=None) == OK
     if NO_GPU:
         assert _quant() == UNS
+
+
+def test_outputs_over_inputs():
+    """Shared bytes are refused before a launch; disjoint columns of one buffer are not, nor the elementwise
+    operators in place."""
+    fine = UNS if NO_GPU else OK
+    if not NO_GPU:
+        pytest.skip("the accepted calls would launch on made-up addresses")
+    row = 96 * 2                                                 # x: 32 columns, y: 64 columns of 96
+    assert _mm(x=X, ldx=96, y=X + 64, ldy=96) == fine
+    assert _mm(x=X + 128, ldx=96, y=X, ldy=96) == fine
+    assert _mm(x=X, ldx=96, y=X + 48, ldy=96) == BAD             # y starts inside x
+    assert _mm(x=X, ldx=96, y=X + 9 * row + 48, ldy=96) == BAD   # only the last row of x
+    assert _mm(x=X, ldx=96, y=X + 10 * row, ldy=96) == fine
+    assert _mm(x=X, ldx=96, y=X + 64, ldy=104) == BAD            # another distance of rows over the same bytes
+    assert _mm(x=X, y=X) == BAD and _mm(y=W) == BAD and _mm(y=W + 4 * 64 * 32 * 2 - 16) == BAD
+    assert _mm(y=W + 4 * 64 * 32 * 2) == fine
+    assert _wgrad(dw=X) == BAD and _wgrad(dw=Y) == BAD and _wgrad(dw=X - 16) == BAD
+    assert _mm8(y=X) == BAD and _mm8(y=W) == BAD
+    assert _quant(q=X) == BAD and _quant(q=X + 4 * 64 * 2 - 16) == BAD and _quant(q=X + 4 * 64 * 2) == fine
+    assert _swiglu(h=X) == fine and _swiglu(h=W) == fine and _swiglu(h=X + 16) == BAD
+    assert _swiglu(h=X, ldh=72) == BAD
+    assert _swiglu_b(dgate=W, dup=Y) == fine and _swiglu_b(dgate=Y, dup=W) == fine and _swiglu_b(dup=X) == fine
+    assert _swiglu_b(dgate=W, dup=W) == BAD and _swiglu_b(dgate=W + 16) == BAD and _swiglu_b(dup=X + 32) == BAD
 
 
 def test_binding_refuses_host_tensors():
