@@ -652,84 +652,45 @@ def moe_quantize_act(x, q, sx, stream=None):
 
 
 # ---------------------------------------------------------------- products by group
-# A decode step's calls run for a few microseconds each, so these wrappers pass plain
-# integers and look each property of a tensor up once (about 6 us a call; 15 with the
-# helpers above).
-_FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
-_HALVES = (torch.bfloat16, torch.float16)
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
-_I8 = (torch.int8,)
-_call_cache = {}
+# A decode step's calls run for a few microseconds each, so the checks and the call of
+# these wrappers are native (csrc/moe_binding.cpp).
+_BOUND = ("moe_grouped_mm", "moe_grouped_wgrad", "moe_swiglu", "moe_swiglu_backward", "moe_quantize_int8",
+          "moe_grouped_mm_int8")
+_native = None
 
 
-def _entry(name: str):
-    """A C entry point of the library (``lib()`` takes a lock and finds the function by name on every call)."""
-    L = _lib
-    if L is None or _call_cache.get("lib") is not L:
+def _binding():
+    """The marshalling module, bound to the loaded library's entry points.  Like the library it is (re)built first
+    when it is missing or older than its sources; without it the call raises."""
+    global _native
+    if _native is None:
+        import importlib.machinery
+        import importlib.util
+
+        from . import build as _build
         L = lib()
-        _call_cache.clear()
-        _call_cache["lib"] = L
-    f = _call_cache.get(name)
-    if f is None:
-        f = _call_cache[name] = getattr(L, name)
-    return f
+        try:
+            path = _build.build_binding()
+        except Exception as e:
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing and could not be built: {e}") from e
+        loader = importlib.machinery.ExtensionFileLoader(__name__ + "._binding", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _BOUND))
+        _native = m
+    return _native
 
 
-def _stream_int(stream, device: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _home(t, name: str) -> int:
-    """The current device, which must be the tensor's."""
-    d = t.get_device()
-    if d < 0:
+def _where(t, name: str, stream):
+    """The current device and the stream to launch on, as integers; the tensor has to be a CUDA one."""
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if d != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return d
-
-
-def _dense(t, name: str, device: int, shape, dtypes) -> int:
-    """Address of a contiguous tensor on `device` of the given shape and one of the types."""
-    if t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on cuda:{device}")
-    if t.shape != shape or t.dtype not in dtypes:
-        _shape(t, name, shape, dtypes)
-    return t.data_ptr()
-
-
-def _rows(t, name: str, device: int, shape, dtypes):
-    """Address and distance of the rows of a matrix on `device` whose rows may lie apart (a slice of a wider buffer)."""
-    if t.get_device() != device or t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix on cuda:{device}")
-    if t.shape != shape or t.dtype not in dtypes:
-        _shape(t, name, shape, dtypes)
-    ld, step = t.stride()
-    if step != 1 and shape[1] != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if shape[0] <= 1:  # one row or none: torch leaves the stride open
-        e = 16 // t.element_size()
-        ld = (shape[1] + e - 1) // e * e
-    return t.data_ptr(), ld
-
-
-def _offsets(offsets, groups: int, device: int):
-    if offsets is None:
-        if groups != 1:
-            raise ValueError("offsets: only one group can go without")
-        return None
-    return _dense(offsets, "offsets", device, (groups + 1,), _I32)
-
-
-def _optional(t, name: str, device: int, shape, dtypes):
-    return None if t is None else _dense(t, name, device, shape, dtypes)
-
-
-def _count(n_rows, device: int):
-    return None if n_rows is None else _dense(n_rows.view(-1), "n_rows", device, (1,), _I32)
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def moe_grouped_mm(x, w, offsets, y, transpose_w: bool = False, accumulate: bool = False, stream=None):
@@ -737,95 +698,57 @@ def moe_grouped_mm(x, w, offsets, y, transpose_w: bool = False, accumulate: bool
     x [R, k], w [G, n, k] (``transpose_w``: [G, k, n], the product with w itself, which is the input gradient of the
     other form), bf16 or f16; y [R, n] of that type or fp32.  Rows of x and y may be slices of wider buffers; rows
     outside the groups are left as they were."""
-    dev, wt = _home(w, "w"), w.dtype
-    if w.dim() != 3 or wt not in _HALVES:
-        raise ValueError(f"w: {tuple(w.shape)} {wt}, expected three dimensions, bf16 or f16")
-    shape = w.shape
-    G, n, k = shape
-    pw = _dense(w, "w", dev, shape, _HALVES)
-    if transpose_w:
-        n, k = k, n
-    R = x.shape[0]
-    px, ldx = _rows(x, "x", dev, (R, k), (wt,))
-    py, ldy = _rows(y, "y", dev, (R, n), (wt, torch.float32))
-    _check(_entry("moe_grouped_mm")(G, R, n, k, _FLOATS[wt], px, ldx, pw, 1 if transpose_w else 0,
-                                    _offsets(offsets, G, dev), py, ldy, _FLOATS[y.dtype], 1 if accumulate else 0,
-                                    _stream_int(stream, dev)), "moe_grouped_mm")
+    device, s = _where(w, "w", stream)
+    st = (_native or _binding()).grouped_mm(x, w, offsets, y, transpose_w, accumulate, device, s)
+    if st:
+        raise MoeError(st, "moe_grouped_mm")
 
 
 def moe_grouped_wgrad(dy, x, offsets, dw, accumulate: bool = False, stream=None):
     """dw[g] (+)= dy[rows of g]^T . x[rows of g]: the weight gradient of ``moe_grouped_mm``.  dy [R, n] and x [R, k]
     bf16 or f16; dw [G, n, k] of that type or fp32; an empty group's gradient is zero."""
-    dev, xt = _home(dw, "dw"), x.dtype
-    if dw.dim() != 3:
-        raise ValueError(f"dw: {tuple(dw.shape)}, expected three dimensions")
-    shape = dw.shape
-    G, n, k = shape
-    R = x.shape[0]
-    px, ldx = _rows(x, "x", dev, (R, k), _HALVES)
-    pdy, lddy = _rows(dy, "dy", dev, (R, n), (xt,))
-    pdw = _dense(dw, "dw", dev, shape, (xt, torch.float32))
-    _check(_entry("moe_grouped_wgrad")(G, R, n, k, _FLOATS[xt], pdy, lddy, px, ldx, _offsets(offsets, G, dev), pdw,
-                                       _FLOATS[dw.dtype], 1 if accumulate else 0, _stream_int(stream, dev)),
-           "moe_grouped_wgrad")
+    device, s = _where(dw, "dw", stream)
+    st = (_native or _binding()).grouped_wgrad(dy, x, offsets, dw, accumulate, device, s)
+    if st:
+        raise MoeError(st, "moe_grouped_wgrad")
 
 
 def moe_swiglu(gate, up, h, coef=None, n_rows=None, stream=None):
     """h = coef * SiLU(gate) * up per row ([R, width], fp32, bf16 or f16; coef fp32 [R] or None).  ``n_rows``: one
     int32 on the device, the rows to compute (e.g. ``offsets[-1:]``); the rows behind are left as they were.  h may
     be gate or up."""
-    dev, shape, t = _home(gate, "gate"), gate.shape, (gate.dtype,)
-    pg, ldg = _rows(gate, "gate", dev, shape, _FLOATS)
-    pu, ldu = _rows(up, "up", dev, shape, t)
-    ph, ldh = _rows(h, "h", dev, shape, t)
-    R, width = shape
-    _check(_entry("moe_swiglu")(R, width, _FLOATS[gate.dtype], pg, ldg, pu, ldu, _optional(coef, "coef", dev, (R,), _F32),
-                                _count(n_rows, dev), ph, ldh, _stream_int(stream, dev)), "moe_swiglu")
+    device, s = _where(gate, "gate", stream)
+    st = (_native or _binding()).swiglu(gate, up, h, coef, n_rows, device, s)
+    if st:
+        raise MoeError(st, "moe_swiglu")
 
 
 def moe_swiglu_backward(dh, gate, up, dgate, dup, coef=None, dcoef=None, n_rows=None, stream=None):
     """The gradients of ``moe_swiglu``: dgate, dup (like gate), and dcoef fp32 [R] when given.  dgate and
     dup may each be one of dh, gate and up itself."""
-    dev, shape, t = _home(gate, "gate"), gate.shape, (gate.dtype,)
-    pg, ldg = _rows(gate, "gate", dev, shape, _FLOATS)
-    pd, ldd = _rows(dh, "dh", dev, shape, t)
-    pu, ldu = _rows(up, "up", dev, shape, t)
-    pdg, lddg = _rows(dgate, "dgate", dev, shape, t)
-    pdu, lddu = _rows(dup, "dup", dev, shape, t)
-    R, width = shape
-    _check(_entry("moe_swiglu_backward")(R, width, _FLOATS[gate.dtype], pd, ldd, pg, ldg, pu, ldu,
-                                         _optional(coef, "coef", dev, (R,), _F32), _count(n_rows, dev), pdg, lddg, pdu,
-                                         lddu, _optional(dcoef, "dcoef", dev, (R,), _F32), _stream_int(stream, dev)),
-           "moe_swiglu_backward")
+    device, s = _where(gate, "gate", stream)
+    st = (_native or _binding()).swiglu_backward(dh, gate, up, dgate, dup, coef, dcoef, n_rows, device, s)
+    if st:
+        raise MoeError(st, "moe_swiglu_backward")
 
 
 def moe_quantize_int8(x, q, sx, n_rows=None, stream=None):
     """int8 codes q [R, k] and fp32 scales sx [R] of the rows of x [R, k] (fp32, bf16 or f16): sx = max|x| * fp32(1/127),
     q the nearest integer of x / sx, ties to even.  Weights [.., n, k] quantise per output channel through a view of
     their rows."""
-    dev = _home(x, "x")
-    px, ldx = _rows(x, "x", dev, x.shape, _FLOATS)
-    R, k = x.shape
-    _check(_entry("moe_quantize_int8")(px, _FLOATS[x.dtype], ldx, R, k, _count(n_rows, dev),
-                                       _dense(q, "q", dev, (R, k), _I8), _dense(sx, "sx", dev, (R,), _F32),
-                                       _stream_int(stream, dev)), "moe_quantize_int8")
+    device, s = _where(x, "x", stream)
+    st = (_native or _binding()).quantize_int8(x, q, sx, n_rows, device, s)
+    if st:
+        raise MoeError(st, "moe_quantize_int8")
 
 
 def moe_grouped_mm_int8(q, sx, w, sw, offsets, y, accumulate: bool = False, stream=None):
     """y[r] (+)= sx[r] sw[g] (q[r] . w[g]^T) with exact integer sums: q [R, k], w [G, n, k] int8, sx [R], sw [G, n]
     fp32, y [R, n] fp32, bf16 or f16; offsets as in ``moe_grouped_mm``."""
-    dev = _home(w, "w")
-    if w.dim() != 3:
-        raise ValueError(f"w: {tuple(w.shape)}, expected three dimensions")
-    shape = w.shape
-    G, n, k = shape
-    R = q.shape[0]
-    pq, psx = _dense(q, "q", dev, (R, k), _I8), _dense(sx, "sx", dev, (R,), _F32)
-    pw, psw = _dense(w, "w", dev, shape, _I8), _dense(sw, "sw", dev, (G, n), _F32)
-    py, ldy = _rows(y, "y", dev, (R, n), _FLOATS)
-    _check(_entry("moe_grouped_mm_int8")(G, R, n, k, pq, psx, pw, psw, _offsets(offsets, G, dev), py, ldy,
-                                         _FLOATS[y.dtype], 1 if accumulate else 0, _stream_int(stream, dev)),
-           "moe_grouped_mm_int8")
+    device, s = _where(w, "w", stream)
+    st = (_native or _binding()).grouped_mm_int8(q, sx, w, sw, offsets, y, accumulate, device, s)
+    if st:
+        raise MoeError(st, "moe_grouped_mm_int8")
 
 
 def device_error(stream=None) -> int:

@@ -1,7 +1,9 @@
 """Builds the in-tree CUDA libraries (sm_100a) with nvcc: ``libmoe_b200.so`` and
 ``libmoe_b200_debug.so``, the same sources compiled with MOE_DEBUG (the
 checking build: table-dependent accesses are checked against their buffers
-and flagged with MOE_DEVERR_BOUNDS)."""
+and flagged with MOE_DEVERR_BOUNDS); and with g++ the Python module that
+marshals the short calls (``moe_binding.cpp``, host code against the installed
+torch, whose version its file name carries)."""
 from __future__ import annotations
 
 import os
@@ -22,6 +24,39 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
+
+
+BINDING_SOURCE = os.path.join(CSRC, "moe_binding.cpp")
+
+
+def binding_path() -> str:
+    import torch
+    version = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(HERE, f"_binding_{version}.so")
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Builds the marshalling module when it is missing or older than its sources; returns its path."""
+    import sysconfig
+
+    import torch
+
+    path = binding_path()
+    deps = [BINDING_SOURCE, os.path.join(HERE, "..", "include", "moe.h")]
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in inc], BINDING_SOURCE,
+           "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, path)
+    return path
 
 
 def _nvcc():
@@ -67,12 +102,13 @@ def _build_variants(variants, verbose: bool, ptxas_verbose: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Builds whichever of the two libraries is missing or older than its sources
-    (both with force); returns the path of the regular one."""
+    """Builds whichever of the two libraries and the marshalling module is missing or
+    older than its sources (all with force); returns the path of the regular library."""
     todo = [(LIB, [], "release"), (LIB_DEBUG, ["-DMOE_DEBUG"], "debug")]
     todo = [v for v in todo if force or _stale(v[0])]
     if todo:
         _build_variants(todo, verbose, ptxas_verbose)
+    build_binding(force, verbose)
     return LIB
 
 

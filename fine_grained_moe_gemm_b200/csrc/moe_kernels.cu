@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "moe_device.cuh"
 #include "moe_gemm.cuh"
@@ -1449,34 +1450,36 @@ static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_
     return cudaLaunchKernelEx(&cfg, kernel, (const RaggedArgs)*args);
 }
 
-int split_clusters(int split) {
-    static std::atomic<int> known[64][SPLIT_MAX_CLUSTER + 1];  // count + 1; 0: not asked yet
+const int* split_clusters() {
+    struct Table {
+        std::once_flag once;
+        int at_once[SPLIT_MAX_CLUSTER + 1] = {};
+    };
+    static Table tables[64];
     int dev = 0;
-    if (split < 1 || split > SPLIT_MAX_CLUSTER || cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
-    int have = known[dev][split].load(std::memory_order_relaxed);
-    if (!have) {  // one CTA an SM: every variant takes more than half of the shared memory
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = 0;
+    Table& t = tables[dev];
+    std::call_once(t.once, [&t] {
         auto kernel = moe_split_kernel<RAG_NT, false>;
-        int n = 0;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = split;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(split);
-        cfg.blockDim = dim3(SPLIT_THREADS);
-        cfg.dynamicSmemBytes = 227 * 1024;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-            cudaGetLastError();  // this size is not used
-            n = 0;
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        for (int split = 1; split <= SPLIT_MAX_CLUSTER; ++split) {
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = split;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(split);
+            cfg.blockDim = dim3(SPLIT_THREADS);
+            cfg.dynamicSmemBytes = 227 * 1024;  // one CTA an SM: every variant takes more than half of its memory
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) t.at_once[split] = n;
         }
-        have = n + 1;
-        known[dev][split].store(have, std::memory_order_relaxed);
-    }
-    return have - 1;
+        cudaGetLastError();  // a size that is refused stays at 0 and is not used
+    });
+    return t.at_once;
 }
 
 cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s) {

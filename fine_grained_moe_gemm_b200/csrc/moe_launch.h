@@ -187,8 +187,8 @@ struct RaggedArgs {
 };
 
 constexpr int SPLIT_MAX_CLUSTER = 16;
-// Clusters of `split` CTAs that run at the same time on the current device (0: none)
-int split_clusters(int split);
+// [split]: clusters of `split` CTAs that run at the same time on the current device (0: none)
+const int* split_clusters();
 cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s);
 cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s);
 

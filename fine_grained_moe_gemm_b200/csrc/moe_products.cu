@@ -126,13 +126,14 @@ ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, i
         offer(true, bn, 1, tiles, sms / 2, kPairClocks, kPairTileClocks);
         if (tiles >= 2 * sms) return best;  // rounds enough for the rest of the last not to matter
     }
+    const int* at_once = split_clusters();
     for (int bn = 128; bn >= (dir == RAG_TN ? 64 : 16); bn /= 2) {
         const long long tiles = columns(bn) * ceil_div(n, 128);
         // parts of four blocks at least: a shorter one is over before its pipeline is full
         for (int split = 1; split <= SPLIT_MAX_CLUSTER && (split == 1 || 4 * split <= blocks); ++split) {
-            const int at_once = split_clusters(split);
-            if (split > 1 && tiles > at_once) break;
-            if (at_once > 0) offer(false, bn, split, tiles, at_once, split > 1 ? kMeetClocks : 0, kSplitTileClocks);
+            if (split > 1 && tiles > at_once[split]) break;
+            if (at_once[split] > 0)
+                offer(false, bn, split, tiles, at_once[split], split > 1 ? kMeetClocks : 0, kSplitTileClocks);
         }
     }
     return best;
