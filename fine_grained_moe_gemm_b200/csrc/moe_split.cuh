@@ -55,6 +55,12 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_
         : "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_id() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -125,7 +131,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     if (warp == 4) tmem_alloc<SPLIT_TMEM_COLS>(tmem_slot);
     const int mt = (P.n + 127) >> 7;
     rag_build_table<SPLIT_THREADS>(P, tab, warp_sums, [&](int rows) {
-        return mt * (DIR == RAG_TN ? (P.k + bn - 1) / bn : (rows + bn - 1) / bn);
+        return mt * rag_chunks<DIR>(P, rows);
     });
     tc_fence_before();
     __syncthreads();
@@ -133,32 +139,34 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     const uint32_t tmem_base = *tmem_slot;
 
     // This cluster's tile.  The grid is an upper bound: clusters behind the last tile leave.
-    const int tile = blockIdx.x / P.split;
+    // (Every division here is on the way to the first load; a run-time one costs about 150 clocks.)
+    const int tile = (int)cluster_id();
     const bool work = tile < tab.first[P.groups];
     int g = 0, f0 = 0, row0 = 0, rows = 0, col0 = 0, width = 0;
     if (work) {
         g = rag_group(tab, P.groups, tile);
         const int local = tile - tab.first[g];
-        const int nc = DIR == RAG_TN ? (P.k + bn - 1) / bn : (tab.count[g] + bn - 1) / bn;
-        const int m = local / nc, c = local - m * nc;  // chunks that share weights run together
-        f0 = m * 128;
         row0 = tab.start[g];
         rows = tab.count[g];
+        const int nc = rag_chunks<DIR>(P, rows);
+        const int m = nc == 1 ? local : local / nc, c = local - m * nc;  // chunks that share weights run together
+        f0 = m * 128;
         if (DIR == RAG_TN) {
             col0 = c * bn;
             width = min(bn, P.k - col0);
         } else {
-            const int w = ((rows + nc - 1) / nc + 15) & ~15;  // equal chunks
+            const int w = nc == 1 ? bn : ((rows + nc - 1) / nc + 15) & ~15;  // equal chunks
             row0 += c * w;
             width = min(w, rows - c * w);
-            if (width < 0) width = 0;
         }
     }
     constexpr int block_k = I8 ? 128 : 64;
     constexpr int seg_blocks = I8 ? 1 << 30 : RAG_SEGMENT / 64;
     const int len = DIR == RAG_TN ? rows : P.k;
-    const int all_blocks = work && width > 0 ? (len + block_k - 1) / block_k : 0;
-    auto split_begin = [&](int blocks, int part) { return (int)((unsigned)blocks * (unsigned)part / (unsigned)P.split); };
+    const int all_blocks = work ? (len + block_k - 1) / block_k : 0;
+    auto split_begin = [&](int blocks, int part) {
+        return P.split == 1 ? blocks * part : (int)((unsigned)blocks * (unsigned)part / (unsigned)P.split);
+    };
     const int kb0 = split_begin(all_blocks, rank), kb1 = split_begin(all_blocks, rank + 1);
     const int mma_n = DIR == RAG_TN ? (width + 63) & ~63 : (width + 15) & ~15;
 
@@ -335,33 +343,39 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     else if (stores) named_bar_sync(1, SPLIT_EPI_WARPS * 32);
     if (stores && !*abort_flag) {
         const uint32_t part = smem_u32(ring);
-        const int t = threadIdx.x - SPLIT_EPI_WARP0 * 32;
         const int n_rows = DIR == RAG_TN ? min(128, P.n - f0) : width;      // rows of the output's tile
         const int n_vec = (DIR == RAG_TN ? width : min(128, P.n - f0)) / 4;  // its pieces of four
         const int pitch = DIR == RAG_TN ? bn + 4 : 128;
-        const int r0 = n_rows * rank / P.split, r1 = n_rows * (rank + 1) / P.split;
-        for (int i = t; i < (r1 - r0) * n_vec; i += SPLIT_EPI_WARPS * 32) {
-            const int r = r0 + i / n_vec, v = i % n_vec;
+        const int r0 = split_begin(n_rows, rank), r1 = split_begin(n_rows, rank + 1);
+        // a lane takes one piece of a row, a warp one row (TN with 64 columns: two)
+        const bool two = DIR == RAG_TN && bn == 64;
+        const int v = two ? lane & 15 : lane;
+        const int w = warp - SPLIT_EPI_WARP0;
+        for (int r = r0 + (two ? 2 * w + (lane >> 4) : w); r < r1 && v < n_vec; r += two ? 2 * SPLIT_EPI_WARPS : SPLIT_EPI_WARPS) {
+            const uint32_t at = (uint32_t)(r * pitch + v * 4) * 4;
             float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             int4 z = make_int4(0, 0, 0, 0);
-            for (int p0 = 0; p0 < P.split; p0 += 8) {
-                float4 u[8];  // loads of eight parts under way together
+            if (P.split == 1) {
+                s = *reinterpret_cast<const float4*>(ring + at);
+                z = make_int4(__float_as_int(s.x), __float_as_int(s.y), __float_as_int(s.z), __float_as_int(s.w));
+            } else {
+                for (int p0 = 0; p0 < P.split; p0 += 8) {  // (a part without blocks is zero)
+                    float4 u[8];                           // loads of eight parts under way together
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    u[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    // parts without blocks (fewer blocks than CTAs) hold nothing
-                    if (p0 + p < P.split && split_begin(all_blocks, p0 + p) < split_begin(all_blocks, p0 + p + 1))
-                        u[p] = ld_cluster_f4(mapa_shared(part + (uint32_t)(r * pitch + v * 4) * 4, (uint32_t)(p0 + p)));
-                }
+                    for (int p = 0; p < 8; ++p) {
+                        u[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (p0 + p < P.split) u[p] = ld_cluster_f4(mapa_shared(part + at, (uint32_t)(p0 + p)));
+                    }
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    if (I8) {
-                        z.x += __float_as_int(u[p].x);
-                        z.y += __float_as_int(u[p].y);
-                        z.z += __float_as_int(u[p].z);
-                        z.w += __float_as_int(u[p].w);
-                    } else {
-                        s = make_float4(s.x + u[p].x, s.y + u[p].y, s.z + u[p].z, s.w + u[p].w);
+                    for (int p = 0; p < 8; ++p) {
+                        if (I8) {
+                            z.x += __float_as_int(u[p].x);
+                            z.y += __float_as_int(u[p].y);
+                            z.z += __float_as_int(u[p].z);
+                            z.w += __float_as_int(u[p].w);
+                        } else {
+                            s = make_float4(s.x + u[p].x, s.y + u[p].y, s.z + u[p].z, s.w + u[p].w);
+                        }
                     }
                 }
             }
