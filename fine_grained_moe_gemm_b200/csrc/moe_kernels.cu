@@ -1380,44 +1380,61 @@ cudaError_t launch_ep_combine(const float* back, const int32_t* send_tok, int n_
     return cudaGetLastError();
 }
 
-template <int DIR, bool I8, bool PROMOTE>
+template <int DIR, bool I8, int MODE>
 static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_t s) {
     constexpr int smem = RagCfg<DIR>::SMEM_BYTES;
-    auto kernel = moe_ragged_kernel<DIR, I8, PROMOTE>;
+    auto kernel = moe_ragged_kernel<DIR, I8, MODE>;
     static std::atomic<bool> attr_set[64];  // once per device (a repeated set is harmless)
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
-        if (PROMOTE) {  // the warps share out the registers of the launch: they must be there
+        if (MODE != RAG_PLAIN) {  // the warps share out the registers of the launch: they must be there
             cudaFuncAttributes fa;
             cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
             if (e != cudaSuccess) return e;
             if (fa.numRegs < RAG_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
         }
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && MODE == RAG_SPLIT)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
     }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = MODE == RAG_SPLIT ? 2 * args->split : 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(RAG_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     note_launch();
-    kernel<<<grid, RAG_THREADS, smem, s>>>(*args);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, *args);
+}
+
+template <int DIR>
+static cudaError_t launch_ragged_dir(const RaggedArgs* args, int grid, cudaStream_t s) {
+    if (args->split > 1) return launch_ragged_t<DIR, false, RAG_SPLIT>(args, grid, s);
+    // fp32 results of sums that may be longer than a segment
+    if (args->out == MOE_F32 && (DIR == RAG_TN ? args->rows : args->k) > RAG_SEGMENT)
+        return launch_ragged_t<DIR, false, RAG_PROMOTE>(args, grid, s);
+    return launch_ragged_t<DIR, false, RAG_PLAIN>(args, grid, s);
 }
 
 cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s) {
-    grid &= ~1;
-    if (grid < 2) return cudaErrorInvalidValue;
-    if (i8) return dir == RAG_NT ? launch_ragged_t<RAG_NT, true, false>(args, grid, s) : cudaErrorInvalidValue;
-    // fp32 results of sums that may be longer than a segment
-    const bool promote = args->out == MOE_F32 && (dir == RAG_TN ? args->rows : args->k) > RAG_SEGMENT;
-    if (dir == RAG_NT)
-        return promote ? launch_ragged_t<RAG_NT, false, true>(args, grid, s)
-                       : launch_ragged_t<RAG_NT, false, false>(args, grid, s);
-    if (dir == RAG_NN)
-        return promote ? launch_ragged_t<RAG_NN, false, true>(args, grid, s)
-                       : launch_ragged_t<RAG_NN, false, false>(args, grid, s);
-    if (dir != RAG_TN) return cudaErrorInvalidValue;
-    return promote ? launch_ragged_t<RAG_TN, false, true>(args, grid, s)
-                   : launch_ragged_t<RAG_TN, false, false>(args, grid, s);
+    if (grid < 2 || args->split < 1 || 2 * args->split > SPLIT_MAX_CLUSTER || grid % (2 * args->split) != 0)
+        return cudaErrorInvalidValue;
+    if (i8 && dir != RAG_NT) return cudaErrorInvalidValue;
+    if (i8)
+        return args->split > 1 ? launch_ragged_t<RAG_NT, true, RAG_SPLIT>(args, grid, s)
+                               : launch_ragged_t<RAG_NT, true, RAG_PLAIN>(args, grid, s);
+    return dir == RAG_NT   ? launch_ragged_dir<RAG_NT>(args, grid, s)
+           : dir == RAG_NN ? launch_ragged_dir<RAG_NN>(args, grid, s)
+           : dir == RAG_TN ? launch_ragged_dir<RAG_TN>(args, grid, s)
+                           : cudaErrorInvalidValue;
 }
 
 template <int DIR, bool I8>

@@ -163,6 +163,7 @@ cudaError_t read_clear_dev_error(unsigned int* flags, cudaStream_t s);
 
 // ---------------------------------------------------------------- products by group (moe_ragged.cuh)
 enum { RAG_NT = 0, RAG_NN = 1, RAG_TN = 2 };
+enum { RAG_PLAIN = 0, RAG_PROMOTE = 1, RAG_SPLIT = 2 };
 constexpr int RAG_MAX_GROUPS = 1024;
 
 struct RaggedArgs {
@@ -179,16 +180,17 @@ struct RaggedArgs {
     int accumulate;
     const float* sx;       // 8-bit operands: scale of each row, and of each [group][n]
     const float* sw;
-    int bn;      // columns of a tile: 256 or 128; moe_split_kernel: 128, 64, 32 or 16 (TN: 128 or 64)
+    int bn;        // columns of a tile: 256 or 128; moe_split_kernel: 128, 64, 32 or 16 (TN: 128 or 64)
     int bn_shift;  // log2 of bn
+    int split;     // CTAs (pairs) of a cluster that share a tile's summed axis
     // moe_split_kernel (b64 is then its only map of the rows, in boxes of bn rows; TN 64 x 64)
-    int split;   // CTAs that share a tile's summed axis
-    int stages;  // of the ring
+    int stages;    // of the ring
 };
 
 constexpr int SPLIT_MAX_CLUSTER = 16;
 // [split]: clusters of `split` CTAs that run at the same time on the current device (0: none)
 const int* split_clusters();
+// grid: CTAs; args->split > 1: one tile for each cluster of 2 * split of them
 cudaError_t launch_ragged(int dir, bool i8, const RaggedArgs* args, int grid, cudaStream_t s);
 cudaError_t launch_split(int dir, bool i8, RaggedArgs* args, long long tiles, cudaStream_t s);
 

@@ -17,8 +17,9 @@ constexpr int kMaxWidth = 65536;     // n, k: 128 * 128 * 65536 = 2^30, so 8-bit
 constexpr int kMaxRows = 1 << 24;    // items of all groups stay inside 32 bits
 constexpr int kMaxQuantWidth = 32768;  // a row in registers: 512 threads of four 16-value pieces
 // Clocks besides the blocks': of a pair kernel's launch and of each of its tiles, of each
-// round of the split kernel (whose CTAs start anew for every tile), of the meeting of parts.
-constexpr int kPairClocks = 6000, kPairTileClocks = 2500, kSplitTileClocks = 8500, kMeetClocks = 1500;
+// round of the split kernel (whose CTAs start anew for every tile), of the meeting of parts
+// and of each of their columns.
+constexpr int kPairClocks = 6000, kPairTileClocks = 2500, kSplitTileClocks = 8500, kMeetClocks = 1500, kMeetColumnClocks = 17;
 constexpr int64_t kMaxLd = 1ll << 36;
 
 int size_of(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
@@ -83,7 +84,8 @@ CUtensorMapDataType map_type(moe_dtype t) {
 
 // Which kernel runs a product, from what the host knows: the sizes, not the offsets.
 //
-// pair: moe_ragged_kernel, tiles of 256 features x bn columns on CTA pairs; else
+// pair: moe_ragged_kernel, tiles of 256 features x bn columns on CTA pairs, with split > 1 the
+// summed axis over that many pairs; else
 // moe_split_kernel, tiles of 128 x bn on single CTAs with the summed axis over `split` of
 // them.  Both take a block of 128 bytes of the summed axis at a time, and a CTA gets about
 // 45 bytes a clock into shared memory, so a block of a tile with c columns a CTA costs
@@ -119,21 +121,28 @@ ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, i
         best.bn = bn;
         best.split = split;
         best.tiles = tiles;
-        best.grid = (int)(2 * tiles < sms ? 2 * tiles : sms);
+        best.grid = (int)(split > 1 ? 2 * split * tiles : 2 * tiles < sms ? 2 * tiles : sms);
     };
     for (int bn = 256; bn >= 128; bn /= 2) {
         const long long tiles = columns(bn) * ceil_div(n, 256);
         offer(true, bn, 1, tiles, sms / 2, kPairClocks, kPairTileClocks);
         if (tiles >= 2 * sms) return best;  // rounds enough for the rest of the last not to matter
     }
+    // a split: parts of four blocks at least (a shorter one is over before its pipeline is full),
+    // and every cluster running at once
     const int* at_once = split_clusters();
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        const long long tiles = columns(bn) * ceil_div(n, 256);
+        for (int split = 2; 2 * split <= SPLIT_MAX_CLUSTER && 4 * split <= blocks && tiles <= at_once[2 * split]; ++split)
+            offer(true, bn, split, tiles, at_once[2 * split], kPairClocks, kPairTileClocks + kMeetClocks + bn * kMeetColumnClocks);
+    }
     for (int bn = 128; bn >= (dir == RAG_TN ? 64 : 16); bn /= 2) {
         const long long tiles = columns(bn) * ceil_div(n, 128);
-        // parts of four blocks at least: a shorter one is over before its pipeline is full
         for (int split = 1; split <= SPLIT_MAX_CLUSTER && (split == 1 || 4 * split <= blocks); ++split) {
             if (split > 1 && tiles > at_once[split]) break;
             if (at_once[split] > 0)
-                offer(false, bn, split, tiles, at_once[split], split > 1 ? kMeetClocks : 0, kSplitTileClocks);
+                offer(false, bn, split, tiles, at_once[split], split > 1 ? kMeetClocks + bn * kMeetColumnClocks : 0,
+                      kSplitTileClocks);
         }
     }
     return best;

@@ -1,7 +1,7 @@
 // The products of moe_ragged.cuh where they have too few tiles to occupy the GPU: few
 // rows, narrow outputs, or a weight gradient of few tiles over many rows.
 //
-// Tiles are smaller (128 features by P.bn <= 128 columns, one CTA each) and the summed
+// Tiles are smaller than there (128 features by P.bn <= 128 columns, one CTA each) and the summed
 // axis is cut over the P.split <= 16 CTAs of a cluster, one tile a cluster.  Each CTA sums its
 // part; the parts meet through distributed shared memory: after a cluster barrier CTA s
 // adds its share of the tile's rows over all parts, in the parts' order, and stores it.
@@ -53,44 +53,6 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_
         "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_id() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Four values of a row, added to what is there with accumulate, rounded once.
-__device__ __forceinline__ void split_store4(const RaggedArgs& P, size_t at, float4 s) {
-    if (P.out == MOE_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(P.y) + at);
-        if (P.accumulate) {
-            const float4 o = *p;
-            s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
-        }
-        *p = s;
-        return;
-    }
-    const int bf16 = P.out == MOE_BF16;
-    uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.y) + at);
-    if (P.accumulate) {
-        const uint2 o = *p;
-        s.x += rag_unpack((uint16_t)o.x, bf16);
-        s.y += rag_unpack((uint16_t)(o.x >> 16), bf16);
-        s.z += rag_unpack((uint16_t)o.y, bf16);
-        s.w += rag_unpack((uint16_t)(o.y >> 16), bf16);
-    }
-    *p = make_uint2(rag_pack2(s.x, s.y, bf16), rag_pack2(s.z, s.w, bf16));
 }
 
 template <int DIR, bool I8>
@@ -342,55 +304,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     if (P.split > 1) cluster_sync_all();
     else if (stores) named_bar_sync(1, SPLIT_EPI_WARPS * 32);
     if (stores && !*abort_flag) {
-        const uint32_t part = smem_u32(ring);
-        const int n_rows = DIR == RAG_TN ? min(128, P.n - f0) : width;      // rows of the output's tile
-        const int n_vec = (DIR == RAG_TN ? width : min(128, P.n - f0)) / 4;  // its pieces of four
-        const int pitch = DIR == RAG_TN ? bn + 4 : 128;
-        const int r0 = split_begin(n_rows, rank), r1 = split_begin(n_rows, rank + 1);
-        // a lane takes one piece of a row, a warp one row (TN with 64 columns: two)
-        const bool two = DIR == RAG_TN && bn == 64;
-        const int v = two ? lane & 15 : lane;
-        const int w = warp - SPLIT_EPI_WARP0;
-        for (int r = r0 + (two ? 2 * w + (lane >> 4) : w); r < r1 && v < n_vec; r += two ? 2 * SPLIT_EPI_WARPS : SPLIT_EPI_WARPS) {
-            const uint32_t at = (uint32_t)(r * pitch + v * 4) * 4;
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            int4 z = make_int4(0, 0, 0, 0);
-            if (P.split == 1) {
-                s = *reinterpret_cast<const float4*>(ring + at);
-                z = make_int4(__float_as_int(s.x), __float_as_int(s.y), __float_as_int(s.z), __float_as_int(s.w));
-            } else {
-                for (int p0 = 0; p0 < P.split; p0 += 8) {  // (a part without blocks is zero)
-                    float4 u[8];                           // loads of eight parts under way together
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        u[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (p0 + p < P.split) u[p] = ld_cluster_f4(mapa_shared(part + at, (uint32_t)(p0 + p)));
-                    }
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        if (I8) {
-                            z.x += __float_as_int(u[p].x);
-                            z.y += __float_as_int(u[p].y);
-                            z.z += __float_as_int(u[p].z);
-                            z.w += __float_as_int(u[p].w);
-                        } else {
-                            s = make_float4(s.x + u[p].x, s.y + u[p].y, s.z + u[p].z, s.w + u[p].w);
-                        }
-                    }
-                }
-            }
-            if (DIR == RAG_TN) {
-                split_store4(P, ((size_t)g * P.n + f0 + r) * P.k + col0 + v * 4, s);
-            } else {
-                if (I8) {
-                    const float sx = __ldg(P.sx + row0 + r);
-                    const float* sw = P.sw + (size_t)g * P.n + f0 + v * 4;
-                    s = make_float4((float)z.x * (sx * __ldg(sw)), (float)z.y * (sx * __ldg(sw + 1)),
-                                    (float)z.z * (sx * __ldg(sw + 2)), (float)z.w * (sx * __ldg(sw + 3)));
-                }
-                split_store4(P, (size_t)(row0 + r) * P.ldy + f0 + v * 4, s);
-            }
-        }
+        rag_store_parts<DIR, I8>(P, ring, 0, 1, rank, warp - SPLIT_EPI_WARP0, g, f0, row0, col0, width);
     }
     __syncwarp();
     if (P.split > 1) cluster_sync_all();  // no CTA leaves while another reads its part

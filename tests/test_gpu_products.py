@@ -225,10 +225,24 @@ def test_mm_one_group_of_few_rows(rows, n, k, transpose):
     _mm_case([rows], n, k, BF, BF if rows % 2 else FS, transpose, seed=rows, first=3, spare=2, accumulate=rows % 3 == 0)
 
 
+@pytest.mark.parametrize("sizes", [[222], [256], [129, 0, 3], [513], [70, 71]])
+@pytest.mark.parametrize("n,k", [(1544, 4104), (392, 18432)])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_mm_few_wide_tiles_over_a_long_axis(sizes, n, k, transpose):
+    _mm_case(sizes, n, k, FH, FH if len(sizes) > 1 else FS, transpose, seed=n, first=1, spare=2, accumulate=len(sizes) == 3)
+
+
 @pytest.mark.parametrize("rows", [1, 15, 16, 63, 64, 65, 257, 1000, 4099])
 @pytest.mark.parametrize("n,k", [(8, 8), (72, 136), (136, 264)])
 def test_wgrad_one_group_of_few_tiles(rows, n, k):
     _wgrad_case([rows], n, k, FH, FH if rows % 2 else FS, seed=rows, first=1, spare=70, accumulate=rows % 3 == 0)
+
+
+@pytest.mark.parametrize("sizes", [[20011], [16384], [9000, 0, 30, 5000], [0, 12345]])
+@pytest.mark.parametrize("n,k", [(552, 488), (264, 1032), (1000, 256)])
+def test_wgrad_few_wide_tiles_of_many_rows(sizes, n, k):
+    _wgrad_case(sizes, n, k, BF, BF if len(sizes) == 4 else FS, seed=n, first=2, spare=70, accumulate=len(sizes) == 2,
+                poison=2 if len(sizes) == 4 else None)
 
 
 def test_wgrad_without_rows_is_zero():
@@ -320,7 +334,7 @@ def _codes(gen, shape):
 @pytest.mark.parametrize("out", [BF, FH, FS])
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("sizes,n,k", [(FEW, 8, 16), (RAGGED, 136, 80), (RAGGED, 264, 1168), (RAGGED, 1032, 208), ([16], 1032, 2064),
-                                       ([16], 136, 18432),
+                                       ([16], 136, 18432), ([250], 1032, 8208), ([100, 90], 392, 16400),
                                        ([300], 256, 128), ([0] * 200 + [1], 64, 32), ([2], 16, 65536)])
 def test_mm_int8(sizes, n, k, accumulate, out):
     gen = _gen(n + k)
