@@ -143,40 +143,77 @@ __device__ __forceinline__ int rag_group(const RagTable& t, int groups, int i) {
     return lo;
 }
 
-// Item i: the group by bisection, then inside it bands of RAG_BAND chunks (TN: column
-// tiles).  A band's chunks run together over the feature tiles, so that at any time the
-// pairs work on a block of about RAG_BAND chunks x 9 tiles whose operands L2 holds.
+// Items in increasing order.  A group's items run in bands of RAG_BAND chunks (TN: column
+// tiles), a band's chunks together over the feature tiles: at any time the pairs work on a
+// block of about RAG_BAND chunks x 9 tiles whose operands L2 holds.
+// What depends on the group is kept from item to item, and the divisions inside it are
+// products with reciprocals: found anew for each item (a bisection and three divisions) an
+// item cost the epilogue 1200 clocks, a quarter of a weight gradient's over 128 rows.
 template <int DIR>
-__device__ __forceinline__ RagItem rag_item(const RaggedArgs& P, const RagTable& t, int i) {
-    const int lo = rag_group(t, P.groups, i);
-    RagItem it;
-    it.g = lo;
-    it.row0 = t.start[lo];
-    it.rows = t.count[lo];
-    const int mt = (P.n + 255) >> 8;
-    const int nc = rag_chunks<DIR>(P, it.rows);
-    int local = i - t.first[lo];
-    int band = 0;
-    if (local >= RAG_BAND * mt) {
-        band = local / (RAG_BAND * mt);
-        local -= band * RAG_BAND * mt;
+struct RagWalk {
+    const RaggedArgs& P;
+    const RagTable& t;
+    int g = -1, next = 0;         // the group and the first item behind it
+    int first, start, count;
+    int nc, w;                    // its chunks, and rows of a chunk
+    float per_chunks;             // one band: 1 / nc
+    int band_items, tail;         // several: items of a full band, chunks of the last
+    float per_band, per_tail;     // and 1 / each
+
+    __device__ __forceinline__ RagWalk(const RaggedArgs& p, const RagTable& table) : P(p), t(table) {}
+
+    // n / d for 0 <= n < 2^20, from inv = 1 / d: n + 1/2 is at least 1 / (2 d) from every
+    // multiple of d, the product off by at most 2^-22 of the quotient
+    static __device__ __forceinline__ int quotient(int n, float inv) { return (int)(((float)n + 0.5f) * inv); }
+
+    __device__ __forceinline__ void enter(int i) {
+        g = g + 1 < P.groups && t.first[g + 2 <= P.groups ? g + 2 : P.groups] > i ? g + 1 : rag_group(t, P.groups, i);
+        first = t.first[g];
+        next = t.first[g + 1];
+        start = t.start[g];
+        count = t.count[g];
+        nc = rag_chunks<DIR>(P, count);
+        w = DIR == RAG_TN || nc == 1 ? P.bn : ((count + nc - 1) / nc + 31) & ~31;  // equal chunks, at most bn rows
+        if (nc <= RAG_BAND) {
+            per_chunks = 1.0f / (float)nc;
+        } else {
+            band_items = RAG_BAND * ((P.n + 255) >> 8);
+            tail = ((nc - 1) & (RAG_BAND - 1)) + 1;
+            per_band = 1.0f / (float)band_items;
+            per_tail = 1.0f / (float)tail;
+        }
     }
-    const int nb = min(RAG_BAND, nc - band * RAG_BAND);
-    it.m = nb == 1 ? local : nb == RAG_BAND ? local / RAG_BAND : local / nb;
-    const int c = band * RAG_BAND + local - it.m * nb;
-    it.chunks = nc;
-    if (DIR == RAG_TN) {
-        it.col0 = c * P.bn;
-        it.width = min(P.bn, P.k - it.col0);
-    } else {
-        const int w = nc == 1 ? P.bn : ((it.rows + nc - 1) / nc + 31) & ~31;  // equal chunks, at most bn rows
-        it.col0 = 0;
-        it.row0 += c * w;
-        it.width = min(w, it.rows - c * w);
-        it.rows = it.width;
+
+    __device__ __forceinline__ RagItem at(int i) {
+        if (i >= next) enter(i);
+        RagItem it;
+        int local = i - first, band = 0;
+        if (nc <= RAG_BAND) {
+            it.m = quotient(local, per_chunks);
+            local -= it.m * nc;
+        } else {
+            band = local < 1 << 20 ? quotient(local, per_band) : local / band_items;
+            local -= band * band_items;
+            const bool full = (band + 1) * RAG_BAND <= nc;
+            it.m = full ? local / RAG_BAND : quotient(local, per_tail);
+            local -= it.m * (full ? RAG_BAND : tail);
+        }
+        const int c = band * RAG_BAND + local;
+        it.g = g;
+        it.chunks = nc;
+        if (DIR == RAG_TN) {
+            it.row0 = start;
+            it.rows = count;
+            it.col0 = c * w;
+            it.width = min(w, P.k - it.col0);
+        } else {
+            it.row0 = start + c * w;
+            it.rows = it.width = min(w, count - c * w);
+            it.col0 = 0;
+        }
+        return it;
     }
-    return it;
-}
+};
 
 // Blocks of 128 bytes (NT; NN, TN: of 64 rows) of the summed axis an item reads.
 template <int DIR, bool I8>
@@ -662,8 +699,9 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 const uint32_t full0 = mapa_shared(smem_u32(full), pair0);
                 const uint32_t landed0 = mapa_shared(smem_u32(landed), crank);
                 RagCursor<ST> at;
+                RagWalk<DIR> walk(P, tab);
                 for (int i = first; i < total; i += n_clusters) {
-                    const RagItem it = rag_item<DIR>(P, tab, i);
+                    const RagItem it = walk.at(i);
                     const int blocks = rag_blocks<DIR, I8>(P, it);
                     const int f0 = it.m * 256 + (int)rank * 128;
                     const int nh = rag_mma_n<DIR>(it) / 2;  // this CTA's columns of the tile
@@ -721,8 +759,9 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 const uint64_t bd0 = DIR == RAG_TN ? smem_desc_mn_sw128(ring_addr + RAG_SLOT)
                                                    : smem_desc_sw128(ring_addr + RAG_SLOT);
                 bool ok = true;
+                RagWalk<DIR> walk(P, tab);
                 for (int i = first; ok && i < total; i += n_clusters) {
-                    const RagItem it = rag_item<DIR>(P, tab, i);
+                    const RagItem it = walk.at(i);
                     const int blocks = rag_blocks<DIR, I8>(P, it);
                     // elements of the summed axis in the last block (TN: rows past it are zero up to a
                     // multiple of 16; NT, NN: the loads filled in zeros)
@@ -773,8 +812,9 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
             RagCursor<ST> at;
             uint32_t ph = 0;  // bit s: phase of the stage's landed and peer_done
             const uint32_t peer0 = mapa_shared(smem_u32(peer_done), pair0);
+            RagWalk<DIR> walk(P, tab);
             for (int i = first; i < total; i += n_clusters) {
-                const RagItem it = rag_item<DIR>(P, tab, i);
+                const RagItem it = walk.at(i);
                 const int blocks = rag_blocks<DIR, I8>(P, it);
                 const int mine = end(blocks) - begin(blocks);
                 if ((it.rows & 15) == 0 || end(blocks) < blocks || mine == 0) {
@@ -833,8 +873,9 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
             acc_phase ^= 1u << buf;
             buf ^= 1;
         };
+        RagWalk<DIR> walk(P, tab);
         for (int i = first; i < total; i += n_clusters) {
-            const RagItem it = rag_item<DIR>(P, tab, i);
+            const RagItem it = walk.at(i);
             const int f0 = it.m * 256 + (int)rank * 128 + q * 32;
             const size_t base = (size_t)it.g * P.n * P.k;  // TN: the group's dw
             if (DIR == RAG_TN && it.rows == 0) {
@@ -973,7 +1014,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
             __syncwarp();
             cluster_sync_all();  // every part is in its CTA's shared memory
             if (first < total && !*abort_flag) {
-                const RagItem it = rag_item<DIR>(P, tab, first);
+                const RagItem it = walk.at(first);
                 if (DIR != RAG_TN || it.rows > 0 || !P.accumulate)
                     rag_store_parts<DIR, I8>(P, ring, (int)rank, 2, part, warp - RAG_EPI_WARP0, it.g,
                                              it.m * 256 + (int)rank * 128, it.row0, it.col0, it.width);
