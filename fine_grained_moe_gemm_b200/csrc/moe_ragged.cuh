@@ -162,8 +162,8 @@ struct RagWalk {
 
     __device__ __forceinline__ RagWalk(const RaggedArgs& p, const RagTable& table) : P(p), t(table) {}
 
-    // n / d for 0 <= n < 2^20, from inv = 1 / d: n + 1/2 is at least 1 / (2 d) from every
-    // multiple of d, the product off by at most 2^-22 of the quotient
+    // n / d for 0 <= n < 2^20, from inv = 1 / d: (n + 1/2) / d is at least 1 / (2 d) from every
+    // integer, and the product (1 / d to two ulps, one rounding) less than 2^-21 of it off
     static __device__ __forceinline__ int quotient(int n, float inv) { return (int)(((float)n + 0.5f) * inv); }
 
     __device__ __forceinline__ void enter(int i) {
@@ -175,12 +175,12 @@ struct RagWalk {
         nc = rag_chunks<DIR>(P, count);
         w = DIR == RAG_TN || nc == 1 ? P.bn : ((count + nc - 1) / nc + 31) & ~31;  // equal chunks, at most bn rows
         if (nc <= RAG_BAND) {
-            per_chunks = 1.0f / (float)nc;
+            per_chunks = __fdividef(1.0f, (float)nc);
         } else {
             band_items = RAG_BAND * ((P.n + 255) >> 8);
             tail = ((nc - 1) & (RAG_BAND - 1)) + 1;
-            per_band = 1.0f / (float)band_items;
-            per_tail = 1.0f / (float)tail;
+            per_band = __fdividef(1.0f, (float)band_items);
+            per_tail = __fdividef(1.0f, (float)tail);
         }
     }
 
