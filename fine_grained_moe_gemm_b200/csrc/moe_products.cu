@@ -85,12 +85,18 @@ CUtensorMapDataType map_type(moe_dtype t) {
 // Which kernel runs a product, from what the host knows: the sizes, not the offsets.
 //
 // pair: moe_ragged_kernel, tiles of 256 features x bn columns on CTA pairs, with split > 1 the
-// summed axis over that many pairs; else
-// moe_split_kernel, tiles of 128 x bn on single CTAs with the summed axis over `split` of
-// them.  Both take a block of 128 bytes of the summed axis at a time, and a CTA gets about
-// 45 bytes a clock into shared memory, so a block of a tile with c columns a CTA costs
-// (128 + c) * 128 / 45 clocks, and a product its rounds of tiles times its blocks.  The
-// cheapest of the choices runs; a split also pays for its meeting.
+// summed axis over that many pairs; else moe_split_kernel, tiles of 128 x bn on single CTAs
+// with the summed axis over `split` of them.  Both take a block of 128 bytes of the summed
+// axis at a time, and a CTA gets about 45 bytes a clock into shared memory, so a block of a
+// tile with c columns a CTA costs (128 + c) * 128 / 45 clocks, and a product its rounds of
+// tiles times its blocks.  The cheapest of the choices runs; a split also pays for its
+// meeting.  Measured (us; the choice first):
+//   222 rows, n 3272, k 18432         four pairs of 256 columns 32, two of 128 44, two CTAs 46, no split 65
+//   16 rows, 7168, 18432, int8        two CTAs of 16 columns 25.5, two pairs 27.5, no split 35
+//   1024 rows, 7168, 2048             pairs of 256 columns 26, of 128 30, single CTAs 56
+//   512 rows in 8 groups, 2048, 1024  pairs of 128 columns 8.8, single CTAs 10.1
+//   1785 rows, 256, 2688              four pairs of 128 11.2, four CTAs 10.9, no split 12.7
+//   gradient 544 x 488, 47337 rows    eight pairs 46, six CTAs 64, pairs without a split 190
 struct ProductPlan {
     bool pair;
     int grid;         // pair: CTAs
@@ -109,12 +115,14 @@ ProductPlan plan_product(int dir, bool i8, int groups, int rows, int n, int k, i
     const int sms = n_sm & ~1;
     const long long mean = ceil_div(rows, groups < rows ? groups : rows);  // rows of a group that has some
     const int blocks = (int)(dir == RAG_TN ? ceil_div(mean, 64) : ceil_div(k, i8 ? 128 : 64));
+    // columns a tile has in fact: no more than a chunk has rows
+    auto wide = [&](int bn) { return dir == RAG_TN || mean >= bn ? bn : (int)((mean + 31) & ~31ll); };
     auto columns = [&](int bn) { return dir == RAG_TN ? groups * ceil_div(k, bn) : chunks_of(groups, rows, bn); };
     ProductPlan best = {};
     double best_cost = 0.0;
     auto offer = [&](bool pair, int bn, int split, long long tiles, int at_once, int once, int each) {
         const double rounds = (double)((tiles + at_once - 1) / at_once);
-        const double cost = once + rounds * ((blocks + split - 1) / split * ((128 + (pair ? bn / 2 : bn)) * 128 / 45) + each);
+        const double cost = once + rounds * ((blocks + split - 1) / split * ((128 + (pair ? wide(bn) / 2 : bn)) * 128 / 45) + each);
         if (best_cost > 0.0 && cost >= best_cost) return;
         best_cost = cost;
         best.pair = pair;
