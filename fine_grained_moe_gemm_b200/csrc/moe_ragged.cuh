@@ -23,6 +23,11 @@
 //
 // Nothing is scheduled on the host: every CTA builds the groups' item counts in
 // shared memory from the offsets and walks the items with the stride of the grid.
+//
+// Measured (B200).  8192^3, one group: bf16 750 us (tensor pipe 98 % active, 1.24 GHz
+// under the power cap), int8 340 us.  256 groups of 4 rows, 7168 -> 2048: 1142 us, HBM at
+// 99 % of the copy rate.  32768 rows in 256 groups, gradients of 2048 x 7168 in bf16: 2089
+// us, bound by storing 7.5 GB.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -9,6 +9,10 @@
 //
 // Sums stay in fp32 registers of the epilogue (segments of RAG_SEGMENT terms, as PROMOTE
 // there) or in 32-bit integers.
+//
+// Measured (B200): 16 rows, 18432 -> 7168 in int8, two CTAs a tile: 26 us, of which the 132
+// MB of weights stream for 20 (6.7 TB/s), 3 pass before the first and 3 after the last; in
+// 56 tiles without a split 35 us.  256 rows in 16 groups, 256 -> 128: 5.7 us, all latency.
 #pragma once
 
 #include "moe_ragged.cuh"

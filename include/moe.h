@@ -17,6 +17,9 @@
  *     section 10 (FP8: E4M3, 1x128 activation tiles, 128x128 weight blocks,
  *     router in higher precision).
  *
+ * Beside the layer: the experts' products as operators of their own, with their
+ * gradients and in 8-bit integers ("products by group" below).
+ *
  * Conventions shared by every entry point
  *   - All array arguments are DEVICE pointers (cudaMalloc'd or torch tensors'
  *     data_ptr), row-major and densely packed, owned by the caller.  The
