@@ -125,7 +125,10 @@ struct Args {
         *p = t->data_ptr();
         return true;
     }
-    bool flag(int i) const { return PyObject_IsTrue(a[i]) == 1; }
+    bool flag(int i, int* v) const {
+        *v = PyObject_IsTrue(a[i]);
+        return *v >= 0;  // else the exception of its __bool__ is set
+    }
     // two or three dimensions whose sizes the C ABI takes as int
     bool sizes(const at::Tensor& t, const char* name, int dims) const {
         if (t.dim() != dims) return refuse(std::string(name) + ": shape " + text(t.sizes()) + ", expected " + std::to_string(dims) + " dimensions");
@@ -164,7 +167,8 @@ PyObject* grouped_mm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!open(a, nargs, 8, &c, &s)) return nullptr;
     const at::Tensor *x = c.tensor(0, "x"), *w = x ? c.tensor(1, "w") : nullptr, *y = w ? c.tensor(3, "y") : nullptr;
     if (!y || !c.sizes(*w, "w", 3) || !c.sizes(*x, "x", 2)) return nullptr;
-    const bool tr = c.flag(4);
+    int tr, acc;
+    if (!c.flag(4, &tr) || !c.flag(5, &acc)) return nullptr;
     const int64_t G = w->size(0), n = w->size(tr ? 2 : 1), k = w->size(tr ? 1 : 2), R = x->size(0);
     const unsigned t = type_of(*w), out = type_of(*y);
     void *px, *pw, *po, *py;
@@ -172,7 +176,6 @@ PyObject* grouped_mm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!c.dense(1, "w", w->sizes(), kHalves, &pw) || !c.rows(0, "x", {R, k}, t, &px, &ldx) ||
         !c.rows(3, "y", {R, n}, t | F32, &py, &ldy) || !c.offsets(2, G, &po))
         return nullptr;
-    const int acc = c.flag(5);
     return call([&] {
         return fn.grouped_mm((int)G, (int)R, (int)n, (int)k, code_of(t), px, ldx, pw, tr, i32(po), py, ldy, code_of(out),
                              acc, s);
@@ -186,6 +189,8 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!open(a, nargs, 7, &c, &s)) return nullptr;
     const at::Tensor *x = c.tensor(1, "x"), *dw = x ? c.tensor(3, "dw") : nullptr;
     if (!dw || !c.sizes(*dw, "dw", 3) || !c.sizes(*x, "x", 2)) return nullptr;
+    int acc;
+    if (!c.flag(4, &acc)) return nullptr;
     const int64_t G = dw->size(0), n = dw->size(1), k = dw->size(2), R = x->size(0);
     const unsigned t = type_of(*x), out = type_of(*dw);
     void *pdy, *px, *po, *pdw;
@@ -193,7 +198,6 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!c.rows(1, "x", {R, k}, kHalves, &px, &ldx) || !c.rows(0, "dy", {R, n}, t, &pdy, &lddy) ||
         !c.dense(3, "dw", dw->sizes(), t | F32, &pdw) || !c.offsets(2, G, &po))
         return nullptr;
-    const int acc = c.flag(4);
     return call([&] {
         return fn.grouped_wgrad((int)G, (int)R, (int)n, (int)k, code_of(t), pdy, lddy, px, ldx, i32(po), pdw, code_of(out),
                                 acc, s);
@@ -268,6 +272,8 @@ PyObject* grouped_mm_int8(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!open(a, nargs, 9, &c, &s)) return nullptr;
     const at::Tensor *q = c.tensor(0, "q"), *w = q ? c.tensor(2, "w") : nullptr, *y = w ? c.tensor(5, "y") : nullptr;
     if (!y || !c.sizes(*w, "w", 3) || !c.sizes(*q, "q", 2)) return nullptr;
+    int acc;
+    if (!c.flag(6, &acc)) return nullptr;
     const int64_t G = w->size(0), n = w->size(1), k = w->size(2), R = q->size(0);
     const unsigned out = type_of(*y);
     void *pq, *psx, *pw, *psw, *po, *py;
@@ -275,7 +281,6 @@ PyObject* grouped_mm_int8(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (!c.dense(0, "q", {R, k}, I8, &pq) || !c.dense(1, "sx", {R}, F32, &psx) || !c.dense(2, "w", w->sizes(), I8, &pw) ||
         !c.dense(3, "sw", {G, n}, F32, &psw) || !c.rows(5, "y", {R, n}, kFloats, &py, &ldy) || !c.offsets(4, G, &po))
         return nullptr;
-    const int acc = c.flag(6);
     return call([&] {
         return fn.grouped_mm_int8((int)G, (int)R, (int)n, (int)k, static_cast<const int8_t*>(pq), f32(psx),
                                   static_cast<const int8_t*>(pw), f32(psw), i32(po), py, ldy, code_of(out), acc, s);

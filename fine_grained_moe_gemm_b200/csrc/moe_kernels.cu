@@ -1493,8 +1493,8 @@ const int* split_clusters() {
             cfg.numAttrs = 1;
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) t.at_once[split] = n;
+            else cudaGetLastError();  // a size that is refused stays at 0 and is not used
         }
-        cudaGetLastError();  // a size that is refused stays at 0 and is not used
     });
     return t.at_once;
 }

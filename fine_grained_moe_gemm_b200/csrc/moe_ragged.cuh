@@ -11,9 +11,9 @@
 // pair, 128 per SM), the ragged row axis (TN: the k axis) is N, up to 256 wide.  A
 // group's rows then cost MMA width only in steps of 32, where rows as M would pad
 // every group to 128 or 256 of them.  A group of more than P.bn rows (256, or 128 where
-// the product has too few tiles for every SM) is cut into equal chunks.  Each SM loads its own 128 features and half of the chunk's rows.
-// An accumulator is 256 TMEM columns, so two fit: the epilogue of one item overlaps
-// the products of the next.
+// the product has too few tiles for every SM) is cut into equal chunks.  Each SM loads
+// its own 128 features and half of the chunk's rows.  An accumulator is 256 TMEM columns,
+// so two fit: the epilogue of one item overlaps the products of the next.
 //
 // NN and TN read operands whose summed axis is the row axis of memory: their tiles
 // are MN-major in shared memory (64 elements of the free axis by 64 of the summed
@@ -48,7 +48,8 @@ constexpr int RAG_BAND = 8;               // chunks whose items run together (L2
 
 // The tensor core cuts each partial sum off instead of rounding it, so a sum of m terms
 // comes out small by about m * 1e-9 of its value (measured: 2.3e-7 at 256 terms, 1.5e-4
-// at 131072).  A 16-bit result does not see that; an fp32 one does.  With PROMOTE the
+// at 131072).  Half a step of bf16 is 3.9e-3 and of f16 4.9e-4, so a 16-bit result keeps
+// its last bit or misses it by a third of a step; an fp32 one does not.  With PROMOTE the
 // tensor core sums RAG_SEGMENT terms at a time and the epilogue adds the segments in
 // fp32 registers, rounding to nearest.
 constexpr int RAG_SEGMENT = 512;
@@ -80,7 +81,6 @@ struct RagItem {
     int width;    // valid columns of the tile: rows of the chunk (TN: columns of dw)
     int chunks;   // chunks of the group that read the same weights
 };
-
 
 struct RagTable {
     int* start;   // [groups] first row
