@@ -19,7 +19,7 @@ constexpr int kMaxQuantWidth = 32768;  // a row in registers: 512 threads of fou
 // Clocks besides the blocks': of a pair kernel's launch and of each of its tiles, of each
 // round of the split kernel (whose CTAs start anew for every tile), of the meeting of parts
 // and of each of their columns.
-constexpr int kPairClocks = 6000, kPairTileClocks = 2500, kSplitTileClocks = 8500, kMeetClocks = 1500, kMeetColumnClocks = 17;
+constexpr int kPairClocks = 6000, kPairTileClocks = 2500, kSplitTileClocks = 8000, kMeetClocks = 1500, kMeetColumnClocks = 17;
 constexpr int64_t kMaxLd = 1ll << 36;
 
 int size_of(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }

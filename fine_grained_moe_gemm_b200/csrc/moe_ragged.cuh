@@ -101,16 +101,23 @@ __device__ __forceinline__ int rag_items_of(const RaggedArgs& P, int rows) {
 // Fills the table from the offsets (all THREADS threads of the CTA; the caller
 // synchronises).  A group whose offsets decrease or leave [0, rows] has no rows and sets
 // MOE_DEVERR_BAD_ROWS.
+// `head` is what rag_first_offsets loaded: the caller does so before everything else, as the
+// loads' latency is most of what a CTA waits for before its first tile.
+__device__ __forceinline__ int2 rag_first_offsets(const RaggedArgs& P) {
+    const int tid = threadIdx.x;
+    return P.offsets && tid < P.groups ? make_int2(__ldg(P.offsets + tid), __ldg(P.offsets + tid + 1)) : make_int2(0, P.rows);
+}
+
 template <int THREADS, typename ItemsOf>
-__device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTable& t, int* warp_sums,
+__device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTable& t, int* warp_sums, int2 head,
                                                 ItemsOf items_of) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (P.groups + THREADS - 1) / THREADS;  // consecutive groups of a thread
     const int g0 = tid * per;
     int sum = 0;
     for (int g = g0; g < min(g0 + per, P.groups); ++g) {
-        int a = 0, b = P.rows;
-        if (P.offsets) {
+        int a = head.x, b = head.y;  // per == 1: the thread's group
+        if (per > 1) {
             a = __ldg(P.offsets + g);
             b = __ldg(P.offsets + g + 1);
         }
@@ -148,6 +155,17 @@ __device__ __forceinline__ int rag_group(const RagTable& t, int groups, int i) {
     return lo;
 }
 
+// n / d for 0 <= n < 2^20, from inv = 1 / d: (n + 1/2) / d is at least 1 / (2 d) from every
+// integer, and the product (1 / d to two ulps, one rounding) less than 2^-21 of it off.
+__device__ __forceinline__ int quotient(int n, float inv) { return (int)(((float)n + 0.5f) * inv); }
+
+// The first of `blocks` < 2^20 blocks that part p of P.split takes: equal shares, the first
+// ones a block longer.
+__device__ __forceinline__ int rag_share(const RaggedArgs& P, int blocks, int p) {
+    const int each = quotient(blocks, __fdividef(1.0f, (float)P.split));
+    return p * each + min(p, blocks - each * P.split);
+}
+
 // Items in increasing order.  A group's items run in bands of RAG_BAND chunks (TN: column
 // tiles), a band's chunks together over the feature tiles: at any time the pairs work on a
 // block of about RAG_BAND chunks x 9 tiles whose operands L2 holds.
@@ -166,10 +184,6 @@ struct RagWalk {
     float per_band, per_tail;     // and 1 / each
 
     __device__ __forceinline__ RagWalk(const RaggedArgs& p, const RagTable& table) : P(p), t(table) {}
-
-    // n / d for 0 <= n < 2^20, from inv = 1 / d: (n + 1/2) / d is at least 1 / (2 d) from every
-    // integer, and the product (1 / d to two ulps, one rounding) less than 2^-21 of it off
-    static __device__ __forceinline__ int quotient(int n, float inv) { return (int)(((float)n + 0.5f) * inv); }
 
     __device__ __forceinline__ void enter(int i) {
         g = g + 1 < P.groups && t.first[g + 2 <= P.groups ? g + 2 : P.groups] > i ? g + 1 : rag_group(t, P.groups, i);
@@ -629,6 +643,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     constexpr bool SPLIT = MODE == RAG_SPLIT;
     constexpr bool PROMOTE = MODE != RAG_PLAIN;  // sums in the epilogue's registers
     constexpr int ST = C::STAGES;
+    const int2 head = rag_first_offsets(P);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = smem;
@@ -672,7 +687,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
         }
     }
     if (warp == 4) tmem_alloc_pair(tmem_slot);
-    rag_build_table<RAG_THREADS>(P, tab, warp_sums, [&](int rows) { return rag_items_of<DIR>(P, rows); });
+    rag_build_table<RAG_THREADS>(P, tab, warp_sums, head, [&](int rows) { return rag_items_of<DIR>(P, rows); });
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers initialised and TMEM allocated
@@ -683,10 +698,8 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     const int n_clusters = SPLIT ? 1 << 30 : gridDim.x >> 1;  // SPLIT: one item at most
     constexpr int seg_blocks = I8 ? 1 << 30 : RAG_SEGMENT / 64;
     // this pair's blocks of an item's
-    auto begin = [&](int blocks) { return SPLIT ? (int)((unsigned)blocks * (unsigned)part / (unsigned)P.split) : 0; };
-    auto end = [&](int blocks) {
-        return SPLIT ? (int)((unsigned)blocks * (unsigned)(part + 1) / (unsigned)P.split) : blocks;
-    };
+    auto begin = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part) : 0; };
+    auto end = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part + 1) : blocks; };
 
     if (warp < RAG_EPI_WARP0) {
         if (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RAG_REGS_CONTROL));

@@ -61,6 +61,7 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_
 
 template <int DIR, bool I8>
 __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __grid_constant__ RaggedArgs P) {
+    const int2 head = rag_first_offsets(P);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = smem;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     }
     if (warp == 4) tmem_alloc<SPLIT_TMEM_COLS>(tmem_slot);
     const int mt = (P.n + 127) >> 7;
-    rag_build_table<SPLIT_THREADS>(P, tab, warp_sums, [&](int rows) {
+    rag_build_table<SPLIT_THREADS>(P, tab, warp_sums, head, [&](int rows) {
         return mt * rag_chunks<DIR>(P, rows);
     });
     tc_fence_before();
@@ -115,7 +116,9 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
         row0 = tab.start[g];
         rows = tab.count[g];
         const int nc = rag_chunks<DIR>(P, rows);
-        const int m = nc == 1 ? local : local / nc, c = local - m * nc;  // chunks that share weights run together
+        // chunks that share weights run together
+        const int m = nc == 1 ? local : local < 1 << 20 ? quotient(local, __fdividef(1.0f, (float)nc)) : local / nc;
+        const int c = local - m * nc;
         f0 = m * 128;
         if (DIR == RAG_TN) {
             col0 = c * bn;
@@ -130,17 +133,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     constexpr int seg_blocks = I8 ? 1 << 30 : RAG_SEGMENT / 64;
     const int len = DIR == RAG_TN ? rows : P.k;
     const int all_blocks = work ? (len + block_k - 1) / block_k : 0;
-    auto split_begin = [&](int blocks, int part) {
-        return P.split == 1 ? blocks * part : (int)((unsigned)blocks * (unsigned)part / (unsigned)P.split);
-    };
-    const int kb0 = split_begin(all_blocks, rank), kb1 = split_begin(all_blocks, rank + 1);
+    const int kb0 = P.split == 1 ? 0 : rag_share(P, all_blocks, rank);
+    const int kb1 = P.split == 1 ? all_blocks : rag_share(P, all_blocks, rank + 1);
     const int mma_n = DIR == RAG_TN ? (width + 63) & ~63 : (width + 15) & ~15;
 
-    float sum[2][32];  // this thread's feature, columns 32 (half + 2 c) + j; integers as bits
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
     const int q = warp & 3, half = (warp - SPLIT_EPI_WARP0) >> 2;
     bool ok = true;
 
@@ -245,6 +241,11 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
         }
     } else if (warp >= SPLIT_EPI_WARP0) {
         // ------------------------------------------------------------ the part's sums
+        float sum[2][32];  // this thread's feature, columns 32 (half + 2 c) + j; integers as bits
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
         int buf = 0;
         uint32_t acc_phase = 0;
         for (int s0 = kb0; s0 < kb1; s0 += min(seg_blocks, kb1 - s0)) {
