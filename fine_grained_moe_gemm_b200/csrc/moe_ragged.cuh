@@ -38,9 +38,12 @@ namespace moe {
 
 constexpr int RAG_SLOT = 128 * 128;       // half of a stage: 128 features (rows) x 128 bytes of the summed axis
 constexpr int RAG_TN_BLOCK = 64 * 128;    // one 64 x 64 block of an MN-major tile
-// Warps: 0-3 load (a thread issues one TMA instruction every few hundred cycles whatever
-// its size, and a block of 64 is consumed in about 700), 4 issues the MMAs, 5 zeroes
-// TN's tail rows, 8-15 are the epilogue (6 and 7 fill up their warpgroup).
+// Warps: 0 and 1 load A, 2 loads B (a thread issues one TMA instruction every few hundred
+// cycles whatever its size, and a block of 64 is consumed in about 700), 4 issues the MMAs,
+// 5 zeroes TN's tail rows, 8-15 are the epilogue (3, 6 and 7 fill up their warpgroups).
+// Every loading warp has bytes in every block: one that only followed the others could fall
+// two rounds of the ring behind, and a wait for a phase of a barrier that is two phases
+// further never ends.
 constexpr int RAG_EPI_WARP0 = 8;
 constexpr int RAG_EPI_WARPS = 8;
 constexpr int RAG_THREADS = (RAG_EPI_WARP0 + RAG_EPI_WARPS) * 32;
@@ -705,12 +708,11 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
         if (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RAG_REGS_CONTROL));
         if (warp < 4) {
             // ---------------------------------------------------- loads (both CTAs)
-            // warp 0: A (NN, TN: its first 64 features), 1: A's other 64, 2: B (TN: its
-            // first 64 columns), 3: B's other 64
-            const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT) || (warp == 3 && DIR == RAG_TN);
+            // warp 0: A (NN, TN: its first 64 features), 1: A's other 64, 2: B
+            const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT);
             if (works && elect_one()) {
                 const bool is_a = warp < 2;
-                const int half = (warp & 1) * 64;
+                const int half = (warp & 1) * 64;  // of A
                 const uint64_t pol_stream = l2_policy_evict_first();
                 const uint64_t pol_keep = l2_policy_evict_last();
                 const uint64_t pol_normal = l2_policy_evict_normal();
@@ -745,10 +747,13 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                             else if (leader) mbar_arrive_expect_tx(&full[at.slot], 2u * bytes);
                         }
                         if (DIR == RAG_TN) {
-                            if (is_a) tma_load_2d_pair(dst, &P.a, f0 + half, it.row0 + kb * 64, bar, policy);
-                            else if (half == 0 || second)
-                                tma_load_2d_pair(dst, &P.b64, it.col0 + (int)rank * nh + half, it.row0 + kb * 64, bar,
-                                                 policy);
+                            if (is_a) {
+                                tma_load_2d_pair(dst, &P.a, f0 + half, it.row0 + kb * 64, bar, policy);
+                            } else {
+                                const int x = it.col0 + (int)rank * nh, y = it.row0 + kb * 64;
+                                tma_load_2d_pair(dst, &P.b64, x, y, bar, policy);
+                                if (second) tma_load_2d_pair(dst + RAG_TN_BLOCK, &P.b64, x + 64, y, bar, policy);
+                            }
                         } else if (!is_a) {
                             tma_load_2d_pair(dst, bmap, kb * (I8 ? 128 : 64), brow, bar, policy);
                         } else if (DIR == RAG_NT) {

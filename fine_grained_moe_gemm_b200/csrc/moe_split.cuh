@@ -19,7 +19,7 @@
 
 namespace moe {
 
-// Warps: 0-3 load, 4 issues the MMAs, 5 zeroes TN's tail rows, 8-15 are the epilogue, as in
+// Warps: 0-2 load, 4 issues the MMAs, 5 zeroes TN's tail rows, 8-15 are the epilogue, as in
 // moe_ragged.cuh.
 constexpr int SPLIT_EPI_WARP0 = 8;
 constexpr int SPLIT_EPI_WARPS = 8;
@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     bool ok = true;
 
     if (warp < 4) {
-        const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT) || (warp == 3 && DIR == RAG_TN);
+        const bool works = warp == 0 || warp == 2 || (warp == 1 && DIR != RAG_NT);
         if (works && elect_one()) {
             const bool is_a = warp < 2;
-            const int half = (warp & 1) * 64;
+            const int half = (warp & 1) * 64;  // of A
             // weights that one chunk reads stream; those of several chunks stay for the others
             const uint64_t policy = DIR == RAG_TN || !is_a ? l2_policy_evict_normal()
                                     : tab.count[g] > bn   ? l2_policy_evict_last() : l2_policy_evict_first();
@@ -159,8 +159,12 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
                 uint64_t* bar = tail ? &landed[slot] : &full[slot];
                 if (warp == 0) mbar_arrive_expect_tx(bar, bytes);
                 if (DIR == RAG_TN) {
-                    if (is_a) tma_load_2d(dst, &P.a, f0 + half, row0 + kb * 64, bar, policy);
-                    else if (half == 0 || second) tma_load_2d(dst, &P.b64, col0 + half, row0 + kb * 64, bar, policy);
+                    if (is_a) {
+                        tma_load_2d(dst, &P.a, f0 + half, row0 + kb * 64, bar, policy);
+                    } else {
+                        tma_load_2d(dst, &P.b64, col0, row0 + kb * 64, bar, policy);
+                        if (second) tma_load_2d(dst + RAG_TN_BLOCK, &P.b64, col0 + 64, row0 + kb * 64, bar, policy);
+                    }
                 } else if (!is_a) {
                     tma_load_2d(dst, &P.b64, kb * block_k, row0, bar, policy);
                 } else if (DIR == RAG_NT) {

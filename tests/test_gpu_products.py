@@ -731,6 +731,28 @@ def test_many_calls_on_several_streams_at_once():
     assert moe.device_error() == 0
 
 
+def test_ten_thousand_launches_of_narrow_tiles():
+    """Tiles of one 64-column block and sums of several rounds of the ring, back to back: no wait may run out and no
+    launch may differ.  (A loading warp without bytes in such tiles once fell two rounds behind and waited for a phase
+    that was over, about once in a million launches.)"""
+    gen = _gen(77)
+    cases = []
+    for sizes, n, k in (([535], 192, 5648), ([700, 3, 1500], 136, 264), ([9000], 72, 64)):
+        dy, x = _rand(gen, (sum(sizes), n), FH), _rand(gen, (sum(sizes), k), FH)
+        cases.append((dy, x, _offsets(sizes), torch.empty((len(sizes), n, k), device=DEV)))
+    for dy, x, off, dw in cases:
+        moe.moe_grouped_wgrad(dy, x, off, dw)
+        want = dw.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(250):
+                moe.moe_grouped_wgrad(dy, x, off, dw)
+        for _ in range(14):
+            g.replay()
+            assert moe.device_error() == 0
+        assert torch.equal(dw, want)
+
+
 def test_binding_refusals_on_the_gpu():
     x, w = torch.zeros((4, 16), dtype=BF, device=DEV), torch.zeros((2, 8, 16), dtype=BF, device=DEV)
     off, y = torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros((4, 8), dtype=BF, device=DEV)
