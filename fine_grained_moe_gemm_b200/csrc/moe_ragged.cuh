@@ -65,12 +65,13 @@ template <int DIR>
 struct RagCfg {
     // a staging tile of the epilogue, per warp: 32 rows of 64 (NT, NN) or 128 bytes
     static constexpr int STAGING = DIR == RAG_TN ? 4096 : 2048;
+    static constexpr int SCALES = DIR == RAG_NT ? 512 : 0;  // int8: the scales of the warp's rows of a tile
     static constexpr int STAGES = DIR == RAG_TN ? 5 : 6;
     static constexpr int RING = STAGES * 2 * RAG_SLOT;
     static constexpr int TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;  // first row, rows, first item of each group
     static constexpr int BARS = 2 * STAGES + (DIR == RAG_TN ? 2 * STAGES : 0) + 5;
     static constexpr int MISC = (BARS * 8 + (2 + RAG_THREADS / 32) * 4 + 15) / 16 * 16;
-    static constexpr int SMEM_BYTES = 1024 + RING + RAG_EPI_WARPS * STAGING + TABLE + MISC;
+    static constexpr int SMEM_BYTES = 1024 + RING + RAG_EPI_WARPS * (STAGING + SCALES) + TABLE + MISC;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -645,6 +646,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     using C = RagCfg<DIR>;
     constexpr bool SPLIT = MODE == RAG_SPLIT;
     constexpr bool PROMOTE = MODE != RAG_PLAIN;  // sums in the epilogue's registers
+    constexpr bool AHEAD = I8 && !PROMOTE;       // the scales are loaded a tile ahead
     constexpr int ST = C::STAGES;
     const int2 head = rag_first_offsets(P);
     extern __shared__ uint8_t smem_raw[];
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     uint8_t* ring = smem;
     uint8_t* staging = smem + C::RING;
     RagTable tab;
-    tab.start = reinterpret_cast<int*>(staging + RAG_EPI_WARPS * C::STAGING);
+    tab.start = reinterpret_cast<int*>(staging + RAG_EPI_WARPS * (C::STAGING + C::SCALES));
     tab.count = tab.start + RAG_MAX_GROUPS;
     tab.first = tab.count + RAG_MAX_GROUPS;
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tab.start) + C::TABLE);
@@ -879,6 +881,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
         const int q = warp & 3;                          // TMEM lane quarter of this warp
         const int half = (warp - RAG_EPI_WARP0) >> 2;
         uint8_t* stage = staging + (warp - RAG_EPI_WARP0) * C::STAGING;
+        float* scales = reinterpret_cast<float*>(staging + RAG_EPI_WARPS * C::STAGING + (warp - RAG_EPI_WARP0) * C::SCALES);
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), pair0);
         uint32_t acc_phase = 0;
         int buf = 0;
@@ -897,8 +900,25 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
             buf ^= 1;
         };
         RagWalk<DIR> walk(P, tab);
+        // The scales of an int8 product come a tile ahead, and reach every lane through shared
+        // memory once a tile: 65536 x 2048 x 128 took 125 us with a load and a meeting of the
+        // warp for each 32 rows, 95 us so (75 us the bf16 product of the same output).
+        RagItem ahead = {};
+        float sw_ahead = 0.0f, sx_ahead[4] = {};
+        auto load_scales = [&](int i) {  // lane l: feature l of the warp, and rows l of its chunks of 32
+            if (i >= total) return;
+            ahead = walk.at(i);
+            const int f = ahead.m * 256 + (int)rank * 128 + q * 32 + lane;
+            if (f < P.n) sw_ahead = __ldg(P.sw + (size_t)ahead.g * P.n + f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int r = 32 * (half + 2 * c) + lane;
+                if (r < ahead.width) sx_ahead[c] = __ldg(P.sx + ahead.row0 + r);
+            }
+        };
+        if (AHEAD) load_scales(first);
         for (int i = first; i < total; i += n_clusters) {
-            const RagItem it = walk.at(i);
+            const RagItem it = AHEAD ? ahead : walk.at(i);
             const int f0 = it.m * 256 + (int)rank * 128 + q * 32;
             const size_t base = (size_t)it.g * P.n * P.k;  // TN: the group's dw
             if (DIR == RAG_TN && it.rows == 0) {
@@ -978,8 +998,13 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 }
                 continue;
             }
-            float sw = 0.0f;
-            if (I8 && f0 + lane < P.n) sw = __ldg(P.sw + (size_t)it.g * P.n + f0 + lane);
+            const float sw = sw_ahead;
+            if (AHEAD) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) scales[32 * c + lane] = sx_ahead[c];
+                __syncwarp();
+                load_scales(i + n_clusters);
+            }
             if (!wait_acc()) break;
             const uint32_t t0 = lanes + (uint32_t)(buf * 256);
             if (DIR == RAG_TN) {
@@ -1009,15 +1034,9 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
             } else {
                 for (int c0 = 32 * half; c0 < it.width && f0 < P.n; c0 += 64) {
                     float v[32];
-                    float sx = 0.0f;
-                    if (I8 && c0 + lane < it.width) sx = __ldg(P.sx + it.row0 + c0 + lane);
                     tmem_ld32(t0 + (uint32_t)c0, v);
                     if (I8) {
-                        // the rows' scales to every lane through the stage, four with one load (with a
-                        // shuffle each 18244 x 6256 x 208 took 109 us instead of 105)
-                        float* st = reinterpret_cast<float*>(stage);
-                        st[lane] = sx;
-                        __syncwarp();
+                        const float* st = scales + (c0 >> 6) * 32;
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const float4 s4 = *reinterpret_cast<const float4*>(st + j);
@@ -1026,7 +1045,6 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                             v[j + 2] = (float)__float_as_int(v[j + 2]) * (s4.z * sw);
                             v[j + 3] = (float)__float_as_int(v[j + 3]) * (s4.w * sw);
                         }
-                        __syncwarp();
                     }
                     rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, v);
                 }
