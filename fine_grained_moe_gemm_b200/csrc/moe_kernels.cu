@@ -1388,7 +1388,7 @@ static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
-        if (MODE != RAG_PLAIN) {  // the warps share out the registers of the launch: they must be there
+        if (MODE != RAG_PLAIN || I8) {  // the warps share out the registers of the launch: they must be there
             cudaFuncAttributes fa;
             cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
             if (e != cudaSuccess) return e;

@@ -56,7 +56,8 @@ constexpr int RAG_BAND = 8;               // chunks whose items run together (L2
 // tensor core sums RAG_SEGMENT terms at a time and the epilogue adds the segments in
 // fp32 registers, rounding to nearest.
 constexpr int RAG_SEGMENT = 512;
-// The segments' sums take 128 registers of an epilogue thread, so PROMOTE moves
+// The segments' sums take 128 registers of an epilogue thread, so PROMOTE (and an int8
+// product, whose scales and next item go along: 2 % on short sums) moves
 // registers from warps 0-7 to warps 8-15: 256 x 56 + 256 x 200 = 512 x 128, the
 // registers that the CTA was launched with (launch_ragged checks that it was).
 constexpr int RAG_REGS_LAUNCH = 128, RAG_REGS_CONTROL = 56, RAG_REGS_EPILOGUE = 200;
@@ -65,7 +66,7 @@ template <int DIR>
 struct RagCfg {
     // a staging tile of the epilogue, per warp: 32 rows of 64 (NT, NN) or 128 bytes
     static constexpr int STAGING = DIR == RAG_TN ? 4096 : 2048;
-    static constexpr int SCALES = DIR == RAG_NT ? 512 : 0;  // int8: the scales of the warp's rows of a tile
+    static constexpr int SCALES = DIR == RAG_NT ? 512 : 0;  // int8: the scales of four chunks of 32 rows, per warp
     static constexpr int STAGES = DIR == RAG_TN ? 5 : 6;
     static constexpr int RING = STAGES * 2 * RAG_SLOT;
     static constexpr int TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;  // first row, rows, first item of each group
@@ -639,6 +640,28 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+__device__ __forceinline__ void rag_arrive(uint32_t bar_cluster, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster), "r"(count) : "memory");
+}
+
+// Whether the two halves of the epilogue's warps take whole tiles in turn, one accumulator
+// each, instead of half of every tile's columns.  After a sum of at most 256 bytes the
+// epilogue is what a tile waits for, and its latencies (the wait, the first load, the
+// hand-over) then run side by side; a group's narrow tiles leave no warp without columns.
+// In turn against halves, in us:
+//   214 groups, 7210 rows, n 3352, k 64     bf16 49.8 / 57.8   fp32 59.4 / 82.1
+//   the same, int8, k 128                   bf16 52.9 / 71.5   fp32 66.6 / 87.4
+//   64 groups, 65536 rows, n 2048, k 64     bf16 74.6 / 87.5   fp32  130 / 143
+//   the same, int8, k 128                   bf16 94.7 / 105    fp32  151 / 159
+//   the same, bf16, k 512                   bf16  136 / 134    fp32  179 / 175
+//   1 group, 65536 rows, n 2048, k 128      bf16 77.8 / 75.1   fp32  122 / 119
+//   8 groups, 4096 rows, n 4096, k 64       fp32 23.2 / 22.4 (3.5 tiles a pair: a last
+//                                           tile's epilogue takes twice as long)
+template <bool I8>
+__device__ __forceinline__ bool rag_alternate(const RaggedArgs& P, int total, int pairs) {
+    return P.groups > 1 && P.k <= (I8 ? 256 : 128) && total >= 6 * pairs;
+}
+
 // MODE: RAG_PLAIN; RAG_PROMOTE, fp32 results of long sums; RAG_SPLIT, one tile a cluster of
 // P.split pairs that share its summed axis (rag_store_parts), where a product has few tiles.
 template <int DIR, bool I8, int MODE>
@@ -647,6 +670,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     constexpr bool SPLIT = MODE == RAG_SPLIT;
     constexpr bool PROMOTE = MODE != RAG_PLAIN;  // sums in the epilogue's registers
     constexpr bool AHEAD = I8 && !PROMOTE;       // the scales are loaded a tile ahead
+    constexpr bool REGS = PROMOTE || I8;         // the epilogue needs more than an equal share of registers
     constexpr int ST = C::STAGES;
     const int2 head = rag_first_offsets(P);
     extern __shared__ uint8_t smem_raw[];
@@ -707,7 +731,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     auto end = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part + 1) : blocks; };
 
     if (warp < RAG_EPI_WARP0) {
-        if (PROMOTE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RAG_REGS_CONTROL));
+        if (REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RAG_REGS_CONTROL));
         if (warp < 4) {
             // ---------------------------------------------------- loads (both CTAs)
             // warp 0: A (NN, TN: its first 64 features), 1: A's other 64, 2: B
@@ -877,14 +901,15 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
         }
     } else {
         // ------------------------------------------------------------ epilogue (both CTAs, own TMEM)
-        if (PROMOTE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RAG_REGS_EPILOGUE));
+        if (REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RAG_REGS_EPILOGUE));
         const int q = warp & 3;                          // TMEM lane quarter of this warp
         const int half = (warp - RAG_EPI_WARP0) >> 2;
         uint8_t* stage = staging + (warp - RAG_EPI_WARP0) * C::STAGING;
         float* scales = reinterpret_cast<float*>(staging + RAG_EPI_WARPS * C::STAGING + (warp - RAG_EPI_WARP0) * C::SCALES);
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), pair0);
         uint32_t acc_phase = 0;
-        int buf = 0;
+        const bool alternate = !PROMOTE && DIR != RAG_TN && rag_alternate<I8>(P, total, n_clusters);
+        int buf = alternate ? half : 0;
         auto wait_acc = [&]() -> bool {
             int got = 0;
             if (lane == 0) got = mbar_wait_bounded(&tfull[buf], (acc_phase >> buf) & 1u, abort_flag) ? 1 : 0;
@@ -895,15 +920,17 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
         auto release_acc = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * 8));
+            if (lane == 0) rag_arrive(tempty0 + (uint32_t)(buf * 8), alternate ? 2u : 1u);  // half the warps: twice each
             acc_phase ^= 1u << buf;
-            buf ^= 1;
+            buf ^= alternate ? 0 : 1;
         };
         RagWalk<DIR> walk(P, tab);
         // The scales of an int8 product come a tile ahead, and reach every lane through shared
         // memory once a tile: 65536 x 2048 x 128 took 125 us with a load and a meeting of the
-        // warp for each 32 rows, 95 us so (75 us the bf16 product of the same output).
+        // warp for each 32 rows, 97 us so (75 us the bf16 product of the same output).
         RagItem ahead = {};
+        const int chunks0 = alternate ? 0 : half;
+        const int item0 = alternate ? first + half * n_clusters : first, item_step = alternate ? 2 * n_clusters : n_clusters;
         float sw_ahead = 0.0f, sx_ahead[4] = {};
         auto load_scales = [&](int i) {  // lane l: feature l of the warp, and rows l of its chunks of 32
             if (i >= total) return;
@@ -912,12 +939,12 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
             if (f < P.n) sw_ahead = __ldg(P.sw + (size_t)ahead.g * P.n + f);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int r = 32 * (half + 2 * c) + lane;
+                const int r = 32 * (chunks0 + 2 * c) + lane;
                 if (r < ahead.width) sx_ahead[c] = __ldg(P.sx + ahead.row0 + r);
             }
         };
-        if (AHEAD) load_scales(first);
-        for (int i = first; i < total; i += n_clusters) {
+        if (AHEAD) load_scales(item0);
+        for (int i = item0; i < total; i += item_step) {
             const RagItem it = AHEAD ? ahead : walk.at(i);
             const int f0 = it.m * 256 + (int)rank * 128 + q * 32;
             const size_t base = (size_t)it.g * P.n * P.k;  // TN: the group's dw
@@ -1003,7 +1030,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
 #pragma unroll
                 for (int c = 0; c < 4; ++c) scales[32 * c + lane] = sx_ahead[c];
                 __syncwarp();
-                load_scales(i + n_clusters);
+                load_scales(i + item_step);
             }
             if (!wait_acc()) break;
             const uint32_t t0 = lanes + (uint32_t)(buf * 256);
@@ -1032,21 +1059,33 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                     if (wide) rag_store_h16_tile(P, stage, base, f0, it.col0 + c0);
                 }
             } else {
-                for (int c0 = 32 * half; c0 < it.width && f0 < P.n; c0 += 64) {
-                    float v[32];
-                    tmem_ld32(t0 + (uint32_t)c0, v);
-                    if (I8) {
-                        const float* st = scales + (c0 >> 6) * 32;
+                for (int h = chunks0;; ++h) {  // the warp's chunks of 32 columns: every other one from h on
+                    for (int c0 = 32 * h; c0 < it.width && f0 < P.n; c0 += 64) {
+                        float v[32];
+                        tmem_ld32(t0 + (uint32_t)c0, v);
+                        if (I8) {
+                            const float* st = scales + (c0 >> 6) * 32;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 s4 = *reinterpret_cast<const float4*>(st + j);
-                            v[j] = (float)__float_as_int(v[j]) * (s4.x * sw);
-                            v[j + 1] = (float)__float_as_int(v[j + 1]) * (s4.y * sw);
-                            v[j + 2] = (float)__float_as_int(v[j + 2]) * (s4.z * sw);
-                            v[j + 3] = (float)__float_as_int(v[j + 3]) * (s4.w * sw);
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 s4 = *reinterpret_cast<const float4*>(st + j);
+                                v[j] = (float)__float_as_int(v[j]) * (s4.x * sw);
+                                v[j + 1] = (float)__float_as_int(v[j + 1]) * (s4.y * sw);
+                                v[j + 2] = (float)__float_as_int(v[j + 2]) * (s4.z * sw);
+                                v[j + 3] = (float)__float_as_int(v[j + 3]) * (s4.w * sw);
+                            }
                         }
+                        rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, v);
                     }
-                    rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, v);
+                    if (!alternate || h == 1) break;
+                    if (AHEAD && it.width > 32) {
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int r = 32 + 64 * c + lane;
+                            if (r < it.width) scales[32 * c + lane] = __ldg(P.sx + it.row0 + r);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             release_acc();

@@ -365,6 +365,23 @@ def test_mm_int8(sizes, n, k, accumulate, out):
     assert torch.equal(y[:first], old[:first]) and torch.equal(y[end:], old[end:])
 
 
+# many groups over short sums: enough tiles that every pair of SMs takes six or more, of all widths
+MANY = [0, 1, 17, 32, 33, 64, 0, 100, 129, 160, 200, 224, 225, 256, 257, 300] * 3
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("k", [8, 64, 72, 128, 136])
+@pytest.mark.parametrize("dtype,out,accumulate", [(BF, BF, False), (FH, FH, True), (BF, FS, False), (FH, FS, True)])
+def test_mm_many_groups_of_short_sums(dtype, out, accumulate, k, transpose):
+    _mm_case(MANY, 4104, k, dtype, out, transpose, seed=k, first=3, spare=5, strided=True, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("out,accumulate", [(BF, False), (FH, True), (FS, False), (FS, True)])
+@pytest.mark.parametrize("k", [16, 112, 128, 240, 256, 272])
+def test_mm_int8_many_groups_of_short_sums(k, out, accumulate):
+    test_mm_int8(MANY, 4104, k, accumulate, out)
+
+
 # ------------------------------------------------------------------ SwiGLU
 def _swiglu_ref(gate, up, coef, dh=None):
     a, b = gate.double(), up.double()
