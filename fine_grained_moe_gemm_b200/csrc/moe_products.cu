@@ -49,6 +49,8 @@ bool same(const Rows& a, const Rows& b) { return a.p == b.p && a.ld == b.ld; }
 bool share(const void* p, size_t bytes, const Rows& r, int rows) {
     return share(Rows{p, (int64_t)bytes, (int64_t)bytes}, Rows{r.p, (rows - 1) * r.ld + r.w, (rows - 1) * r.ld + r.w}, 1);
 }
+// the same of a vector that may be absent (offsets, scales, coefficients, a count)
+bool vector_in(const void* p, int64_t count, const Rows& r, int rows) { return p && share(p, (size_t)count * 4, r, rows); }
 
 // Shapes and flags that every product checks; k_step: elements of 16 bytes of the operands.
 moe_status check_product(int groups, int rows, int n, int k, int k_step, const int32_t* offsets, moe_dtype out,
@@ -215,7 +217,8 @@ moe_status moe_grouped_mm(int groups, int rows, int n, int k, moe_dtype dtype, c
     if (!x || !w || !y || !aligned16(x) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
     if (!good_ld(ldx, k, 2) || !good_ld(ldy, n, size_of(y_dtype))) return MOE_ERR_INVALID_ARG;
     const Rows rx = {x, ldx * 2, k * 2}, ry = {y, ldy * size_of(y_dtype), n * size_of(y_dtype)};
-    if (share(rx, ry, rows) || share(w, (size_t)groups * n * k * 2, ry, rows)) return MOE_ERR_INVALID_ARG;
+    if (share(rx, ry, rows) || share(w, (size_t)groups * n * k * 2, ry, rows) || vector_in(offsets, groups + 1, ry, rows))
+        return MOE_ERR_INVALID_ARG;
     return product(false, dtype, groups, rows, n, k, x, ldx, w, transpose_w, nullptr, nullptr, offsets, y, ldy,
                    y_dtype, accumulate, stream);
 }
@@ -231,7 +234,9 @@ moe_status moe_grouped_mm_int8(int groups, int rows, int n, int k, const int8_t*
         !aligned4(sw) || !good_ld(ldy, n, size_of(y_dtype)))
         return MOE_ERR_INVALID_ARG;
     const Rows rq = {q, k, k}, ry = {y, ldy * size_of(y_dtype), n * size_of(y_dtype)};
-    if (share(rq, ry, rows) || share(w, (size_t)groups * n * k, ry, rows)) return MOE_ERR_INVALID_ARG;
+    if (share(rq, ry, rows) || share(w, (size_t)groups * n * k, ry, rows) || vector_in(offsets, groups + 1, ry, rows) ||
+        vector_in(sx, rows, ry, rows) || vector_in(sw, (int64_t)groups * n, ry, rows))
+        return MOE_ERR_INVALID_ARG;
     return product(true, y_dtype, groups, rows, n, k, q, k, w, 0, sx, sw, offsets, y, ldy, y_dtype, accumulate, stream);
 }
 
@@ -248,6 +253,7 @@ moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dtype dtype
     const size_t dw_bytes = (size_t)groups * n * k * size_of(dw_dtype);
     if (rows && (share(dw, dw_bytes, Rows{dy, lddy * 2, n * 2}, rows) || share(dw, dw_bytes, Rows{x, ldx * 2, k * 2}, rows)))
         return MOE_ERR_INVALID_ARG;
+    if (vector_in(offsets, groups + 1, Rows{dw, (int64_t)dw_bytes, (int64_t)dw_bytes}, 1)) return MOE_ERR_INVALID_ARG;
     DevInfo di;
     if ((st = check_device(&di)) != MOE_OK) return st;
     if (rows == 0) {  // a sum of nothing
@@ -286,6 +292,7 @@ moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* gate, in
     const int64_t wide = (int64_t)width * e;
     const Rows rg = {gate, ld_gate * e, wide}, ru = {up, ld_up * e, wide}, rh = {h, ld_h * e, wide};
     if ((share(rg, rh, rows) && !same(rg, rh)) || (share(ru, rh, rows) && !same(ru, rh))) return MOE_ERR_INVALID_ARG;
+    if (vector_in(coef, rows, rh, rows) || vector_in(n_rows, 1, rh, rows)) return MOE_ERR_INVALID_ARG;
     DevInfo di;
     const moe_status st = check_device(&di);
     if (st != MOE_OK) return st;
@@ -325,6 +332,15 @@ moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, const void*
     for (const Rows& i : in)
         for (const Rows& o : out)
             if (share(i, o, rows) && !same(i, o)) return MOE_ERR_INVALID_ARG;
+    for (const Rows& o : out)
+        if (vector_in(coef, rows, o, rows) || vector_in(n_rows, 1, o, rows) || vector_in(dcoef, rows, o, rows))
+            return MOE_ERR_INVALID_ARG;
+    if (dcoef) {  // may be coef itself: a row's threads have read it before its sum is complete
+        const Rows rc = {dcoef, (int64_t)rows * 4, (int64_t)rows * 4};
+        for (const Rows& i : in)
+            if (vector_in(dcoef, rows, i, rows)) return MOE_ERR_INVALID_ARG;
+        if ((coef != dcoef && vector_in(coef, rows, rc, 1)) || vector_in(n_rows, 1, rc, 1)) return MOE_ERR_INVALID_ARG;
+    }
     DevInfo di;
     const moe_status st = check_device(&di);
     if (st != MOE_OK) return st;
@@ -357,7 +373,10 @@ moe_status moe_quantize_int8(const void* x, moe_dtype dtype, int64_t ldx, int ro
     if (!x || !q || !sx || !aligned16(x) || !aligned16(q) || !aligned4(sx) || !aligned4(n_rows) ||
         !good_ld(ldx, k, size_of(dtype)))
         return MOE_ERR_INVALID_ARG;
-    if (share(q, (size_t)rows * k, Rows{x, ldx * size_of(dtype), (int64_t)k * size_of(dtype)}, rows))
+    const Rows rx = {x, ldx * size_of(dtype), (int64_t)k * size_of(dtype)}, rq = {q, k, k};
+    const Rows rs = {sx, (int64_t)rows * 4, (int64_t)rows * 4};
+    if (share(q, (size_t)rows * k, rx, rows) || vector_in(sx, rows, rx, rows) || vector_in(sx, rows, rq, rows) ||
+        vector_in(n_rows, 1, rq, rows) || vector_in(n_rows, 1, rs, 1))
         return MOE_ERR_INVALID_ARG;
     DevInfo di;
     const moe_status st = check_device(&di);

@@ -345,8 +345,8 @@ MOE_API moe_status moe_dense_ffn(int d, int hidden, moe_dtype act_dtype, moe_dty
  *   - ld*: elements from one row to the next, at least the row, a multiple of 16
  *     bytes; so halves of a wider buffer can be read and written in place.  Weights
  *     and their gradients are dense.
- *   - Outputs may not share bytes with inputs (MOE_ERR_INVALID_ARG; disjoint columns of
- *     one buffer are fine).  One launch, no workspace, results that do
+ *   - Outputs may not share bytes with inputs or with each other (MOE_ERR_INVALID_ARG;
+ *     disjoint columns of one buffer are fine, a vector between the rows is not).  One launch, no workspace, results that do
  *     not depend on the run; sums in fp32 (8-bit operands: exact in 32 bits),
  *     rounded once.  accumulate = 1 adds to the output, before that rounding. */
 
@@ -384,8 +384,8 @@ MOE_API moe_status moe_swiglu(int rows, int width, moe_dtype dtype, const void* 
 /* The gradients of moe_swiglu from dh: with s = sigmoid(gate), a = gate * s
  *   dgate = coef * dh * up * (s + a * (1 - s)),  dup = coef * dh * a,
  *   dcoef[r] = sum over the row of dh * a * up     fp32 [rows], or NULL
- * dgate and dup may each be one of dh, gate and up itself, not the same one; else they
- * share no bytes with them.  The sum has a fixed order. */
+ * dgate and dup may each be one of dh, gate and up itself, not the same one, and dcoef
+ * may be coef; else they share no bytes with the inputs.  The sum has a fixed order. */
 MOE_API moe_status moe_swiglu_backward(int rows, int width, moe_dtype dtype, const void* dh, int64_t ld_dh,
                                        const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
                                        const float* coef, const int32_t* n_rows, void* dgate, int64_t ld_dgate,

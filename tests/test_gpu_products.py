@@ -460,6 +460,18 @@ def test_swiglu_against_differences():
             40 * 2.0 ** -20 * 64 / step * dh.double().abs().amax(1) + 1e-6)
 
 
+@pytest.mark.parametrize("width", [24, 256, 8192])
+def test_coefficient_gradient_in_place(width):
+    gen = _gen(width)
+    g, u, d = (_rand(gen, (300, width), BF) for _ in range(3))
+    c = torch.rand(300, generator=gen, device=DEV)
+    dg, du, dc = torch.empty_like(g), torch.empty_like(g), torch.empty_like(c)
+    moe.moe_swiglu_backward(d, g, u, dg, du, coef=c, dcoef=dc)
+    over = c.clone()
+    moe.moe_swiglu_backward(d, g, u, g, u, coef=over, dcoef=over)
+    assert torch.equal(over, dc) and torch.equal(g, dg) and torch.equal(u, du)
+
+
 @pytest.mark.parametrize("count", [0, 1, 5, 12])
 def test_rows_behind_the_count_stay(count):
     gen = _gen(count)

@@ -147,6 +147,21 @@ def test_outputs_over_inputs():
     assert _swiglu_b(dgate=W, dup=W) == BAD and _swiglu_b(dgate=W + 16) == BAD and _swiglu_b(dup=X + 32) == BAD
 
 
+def test_outputs_over_vectors():
+    """The offsets, scales, coefficients and counts are inputs too."""
+    if not NO_GPU:
+        pytest.skip("the accepted calls would launch on made-up addresses")
+    assert _mm(off=Y + 16) == BAD and _mm(off=Y - 16) == BAD and _mm(off=Y - 20) == UNS   # five offsets
+    assert _wgrad(off=W) == BAD and _wgrad(off=W + 4 * 64 * 32 * 4 - 4) == BAD and _wgrad(off=W + 4 * 64 * 32 * 4) == UNS
+    assert _mm8(off=Y) == BAD and _mm8(sx=Y) == BAD and _mm8(sw=Y - 4 * 4 * 64 + 4) == BAD and _mm8(sw=Y - 4 * 4 * 64) == UNS
+    assert _swiglu(coef=Y + 4 * 64 * 2 - 4) == BAD and _swiglu(n=Y) == BAD and _swiglu(coef=Y - 16, n=Y - 4) == UNS
+    assert _swiglu_b(coef=Z) == BAD and _swiglu_b(n=V) == BAD and _swiglu_b(dcoef=V) == BAD and _swiglu_b(dcoef=Z) == BAD
+    assert _swiglu_b(dcoef=X) == BAD and _swiglu_b(dcoef=W) == BAD and _swiglu_b(dcoef=Y) == BAD
+    assert _swiglu_b(coef=16, dcoef=20) == BAD and _swiglu_b(n=16, dcoef=16) == BAD
+    assert _swiglu_b(coef=16, dcoef=16) == UNS and _swiglu_b(coef=16, dcoef=32) == UNS
+    assert _quant(sx=X) == BAD and _quant(sx=Y) == BAD and _quant(n=Y) == BAD and _quant(n=28) == BAD and _quant(n=32) == UNS
+
+
 def test_binding_refuses_host_tensors():
     x, w, y = torch.zeros(4, 16).bfloat16(), torch.zeros(2, 8, 16).bfloat16(), torch.zeros(4, 8)
     off = torch.zeros(3, dtype=torch.int32)
