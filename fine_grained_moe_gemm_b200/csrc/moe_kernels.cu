@@ -1418,9 +1418,10 @@ static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_
 template <int DIR>
 static cudaError_t launch_ragged_dir(const RaggedArgs* args, int grid, cudaStream_t s) {
     if (args->split > 1) return launch_ragged_t<DIR, false, RAG_SPLIT>(args, grid, s);
-    // fp32 results of sums that may be longer than a segment
-    if (args->out == MOE_F32 && (DIR == RAG_TN ? args->rows : args->k) > RAG_SEGMENT)
-        return launch_ragged_t<DIR, false, RAG_PROMOTE>(args, grid, s);
+    // sums that may be longer than the tensor core may sum alone
+    const int longest = DIR == RAG_TN ? args->rows : args->k;
+    if (args->out == MOE_F32 && longest > RAG_SEGMENT) return launch_ragged_t<DIR, false, RAG_PROMOTE>(args, grid, s);
+    if (args->out != MOE_F32 && longest > args->whole * 64) return launch_ragged_t<DIR, false, RAG_LONG>(args, grid, s);
     return launch_ragged_t<DIR, false, RAG_PLAIN>(args, grid, s);
 }
 

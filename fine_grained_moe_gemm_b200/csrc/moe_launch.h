@@ -163,7 +163,7 @@ cudaError_t read_clear_dev_error(unsigned int* flags, cudaStream_t s);
 
 // ---------------------------------------------------------------- products by group (moe_ragged.cuh)
 enum { RAG_NT = 0, RAG_NN = 1, RAG_TN = 2 };
-enum { RAG_PLAIN = 0, RAG_PROMOTE = 1, RAG_SPLIT = 2 };
+enum { RAG_PLAIN = 0, RAG_PROMOTE = 1, RAG_SPLIT = 2, RAG_LONG = 3 };
 constexpr int RAG_MAX_GROUPS = 1024;
 
 struct RaggedArgs {
@@ -183,6 +183,7 @@ struct RaggedArgs {
     int bn;        // columns of a tile: 256 or 128; moe_split_kernel: 128, 64, 32 or 16 (TN: 128 or 64)
     int bn_shift;  // log2 of bn
     int split;     // CTAs (pairs) of a cluster that share a tile's summed axis
+    int whole;     // RAG_LONG: blocks of 64 terms that the tensor core may sum alone
     // moe_split_kernel (b64 is then its only map of the rows, in boxes of bn rows; TN 64 x 64)
     int stages;    // of the ring
 };

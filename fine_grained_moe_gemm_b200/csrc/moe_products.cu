@@ -20,6 +20,9 @@ constexpr int kMaxQuantWidth = 32768;  // a row in registers: 512 threads of fou
 // round of the split kernel (whose CTAs start anew for every tile), of the meeting of parts
 // and of each of their columns.
 constexpr int kPairClocks = 6000, kPairTileClocks = 2500, kSplitTileClocks = 8000, kMeetClocks = 1500, kMeetColumnClocks = 17;
+// Terms that the tensor core may sum alone for a 16-bit result: it then comes out small by at most
+// 2^-27 of its value a term, an eighth of its half step (2^-11 and 2^-8).
+constexpr int kWholeF16 = 1 << 13, kWholeBF16 = 1 << 16;
 constexpr int64_t kMaxLd = 1ll << 36;
 
 int size_of(moe_dtype t) { return t == MOE_F32 ? 4 : 2; }
@@ -162,6 +165,7 @@ moe_status run_product(int dir, bool i8, RaggedArgs* a, const ProductPlan& p, cu
     a->bn = p.bn;
     while ((1 << a->bn_shift) < p.bn) ++a->bn_shift;
     a->split = p.split;
+    a->whole = (a->out == MOE_F16 ? kWholeF16 : kWholeBF16) / 64;
     return cuda_status(p.pair ? launch_ragged(dir, i8, a, p.grid, s) : launch_split(dir, i8, a, p.tiles, s));
 }
 

@@ -49,12 +49,14 @@ constexpr int RAG_EPI_WARPS = 8;
 constexpr int RAG_THREADS = (RAG_EPI_WARP0 + RAG_EPI_WARPS) * 32;
 constexpr int RAG_BAND = 8;               // chunks whose items run together (L2)
 
-// The tensor core cuts each partial sum off instead of rounding it, so a sum of m terms
-// comes out small by about m * 1e-9 of its value (measured: 2.3e-7 at 256 terms, 1.5e-4
-// at 131072).  Half a step of bf16 is 3.9e-3 and of f16 4.9e-4, so a 16-bit result keeps
-// its last bit or misses it by a third of a step; an fp32 one does not.  With PROMOTE the
-// tensor core sums RAG_SEGMENT terms at a time and the epilogue adds the segments in
-// fp32 registers, rounding to nearest.
+// The tensor core cuts each partial sum off instead of rounding it: after every 16 terms a sum
+// loses up to 2^-23 of its value, always towards zero, so m terms of one sign come out small by up
+// to m * 2^-27 (measured: 6.4e-9 m, 6.7e-3 at 2^20 terms; terms of both signs about a sixth).
+// With PROMOTE the tensor core sums RAG_SEGMENT terms at a time and the epilogue adds the
+// segments in fp32 registers, rounding to nearest.  fp32 results take segments always, 16-bit
+// ones (RAG_LONG) in the groups where the loss could pass an eighth of their half step: segments
+// everywhere cost gradients of short groups their speed (32768 rows in 256 groups, 2048 x 7168 in
+// bf16: 2700 us, 2080 without).
 constexpr int RAG_SEGMENT = 512;
 // The segments' sums take 128 registers of an epilogue thread, so PROMOTE (and an int8
 // product, whose scales and next item go along: 2 % on short sums) moves
@@ -440,6 +442,13 @@ __device__ __forceinline__ void rag_stage_piece(uint8_t* stage, int piece, uint4
     const int lane = threadIdx.x & 31;
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
 }
+// 32 columns of the lane's row in 16 bits, from piece p0 on
+__device__ __forceinline__ void rag_stage_h16(uint8_t* stage, int p0, const float (&v)[32], int bf16) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        rag_stage_piece(stage, p0 + p, make_uint4(rag_pack2(v[8 * p], v[8 * p + 1], bf16), rag_pack2(v[8 * p + 2], v[8 * p + 3], bf16),
+                                                  rag_pack2(v[8 * p + 4], v[8 * p + 5], bf16), rag_pack2(v[8 * p + 6], v[8 * p + 7], bf16)));
+}
 __device__ __forceinline__ uint4 rag_staged(const uint8_t* stage, int row, int piece) {
     return *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
 }
@@ -662,8 +671,9 @@ __device__ __forceinline__ bool rag_alternate(const RaggedArgs& P, int total, in
     return P.groups > 1 && P.k <= (I8 ? 256 : 128) && total >= 6 * pairs;
 }
 
-// MODE: RAG_PLAIN; RAG_PROMOTE, fp32 results of long sums; RAG_SPLIT, one tile a cluster of
-// P.split pairs that share its summed axis (rag_store_parts), where a product has few tiles.
+// MODE: RAG_PLAIN; RAG_PROMOTE, fp32 results of long sums; RAG_LONG, 16-bit results of sums of
+// which some are longer than P.whole blocks; RAG_SPLIT, one tile a cluster of P.split pairs that
+// share its summed axis (rag_store_parts), where a product has few tiles.
 template <int DIR, bool I8, int MODE>
 __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid_constant__ RaggedArgs P) {
     using C = RagCfg<DIR>;
@@ -729,6 +739,8 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     // this pair's blocks of an item's
     auto begin = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part) : 0; };
     auto end = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part + 1) : blocks; };
+    // whether the epilogue adds up an item's segments
+    auto segmented = [&](int blocks) { return MODE == RAG_LONG ? blocks > P.whole : PROMOTE; };
 
     if (warp < RAG_EPI_WARP0) {
         if (REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RAG_REGS_CONTROL));
@@ -818,7 +830,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                     const uint32_t idesc = rag_idesc<DIR, I8>((uint32_t)P.bf16, 256, (uint32_t)rag_mma_n<DIR>(it));
                     const int stop = end(blocks);
                     for (int kb0 = begin(blocks), kb1; kb0 < stop; kb0 = kb1) {
-                        kb1 = PROMOTE ? kb0 + min(seg_blocks, stop - kb0) : blocks;
+                        kb1 = segmented(blocks) ? kb0 + min(seg_blocks, stop - kb0) : stop;
                         if (!mbar_wait_bounded(&tempty[buf], ((acc_phase >> buf) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
                         const uint32_t d = tmem_base + (uint32_t)(buf * 256);
                         for (int kb = kb0; kb < kb1; ++kb) {
@@ -962,8 +974,11 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 if (!SPLIT) continue;  // (SPLIT: the parts are zero)
             }
             const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
-            if (PROMOTE) {
-                // this warp's columns: chunks of 32 at 32 (half + 2 c)
+            if (segmented(rag_blocks<DIR, I8>(P, it))) {
+                // this warp's columns: chunks of 32, every other one; two neighbours where a stored
+                // piece is 64 columns
+                const bool pieces64 = DIR == RAG_TN && MODE == RAG_LONG && !P.accumulate;
+                auto column = [&](int c) { return pieces64 ? 128 * (c >> 1) + 64 * half + 32 * (c & 1) : 32 * (half + 2 * c); };
                 const int blocks = rag_blocks<DIR, I8>(P, it), mine = end(blocks) - begin(blocks);
                 const int segs = I8 ? (mine > 0 ? 1 : 0) : (mine + seg_blocks - 1) / seg_blocks;
                 float sum[4][32];
@@ -976,7 +991,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                     if (!wait_acc()) { ok = false; break; }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int c0 = 32 * (half + 2 * c);
+                        const int c0 = column(c);
                         if (c0 < it.width) {
                             float v[32];
                             tmem_ld32(lanes + (uint32_t)(buf * 256 + c0), v);
@@ -1016,10 +1031,19 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int c0 = 32 * (half + 2 * c);
+                        const int c0 = column(c);
                         if (c0 < it.width) {
-                            if (DIR == RAG_TN) rag_store_f32_tile<true>(P, stage, base, f0, it.col0 + c0, sum[c]);
-                            else rag_store_rows_f32(P, stage, it.row0 + c0, it.width - c0, f0, sum[c]);
+                            if (DIR != RAG_TN) {
+                                if (MODE == RAG_LONG) rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, sum[c]);
+                                else rag_store_rows_f32(P, stage, it.row0 + c0, it.width - c0, f0, sum[c]);
+                            } else if (MODE == RAG_PROMOTE) {
+                                rag_store_f32_tile<true>(P, stage, base, f0, it.col0 + c0, sum[c]);
+                            } else if (P.accumulate) {
+                                rag_store_f32_tile<false>(P, stage, base, f0, it.col0 + c0, sum[c]);
+                            } else {  // a piece is two chunks, or the tile ends in its first
+                                rag_stage_h16(stage, 4 * (c & 1), sum[c], P.out == MOE_BF16);
+                                if ((c & 1) || c0 + 32 >= it.width) rag_store_h16_tile(P, stage, base, f0, it.col0 + (c0 & ~63));
+                            }
                         }
                     }
                 }
@@ -1042,14 +1066,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                     for (int h = 0; h < 2; ++h) {
                         tmem_ld32(t0 + (uint32_t)(c0 + 32 * h), v);
                         if (wide) {
-                            const int bf16 = P.out == MOE_BF16;
-#pragma unroll
-                            for (int p = 0; p < 4; ++p)
-                                rag_stage_piece(stage, 4 * h + p,
-                                                make_uint4(rag_pack2(v[8 * p], v[8 * p + 1], bf16),
-                                                           rag_pack2(v[8 * p + 2], v[8 * p + 3], bf16),
-                                                           rag_pack2(v[8 * p + 4], v[8 * p + 5], bf16),
-                                                           rag_pack2(v[8 * p + 6], v[8 * p + 7], bf16)));
+                            rag_stage_h16(stage, 4 * h, v, P.out == MOE_BF16);
                         } else if (P.out == MOE_F32) {
                             rag_store_f32_tile<true>(P, stage, base, f0, it.col0 + c0 + 32 * h, v);
                         } else {

@@ -1,0 +1,109 @@
+"""Long sums of the products by group, held to bounds that a lost block, a lost row or a bias would break.
+
+Tolerances of the sums of one sign.  After every 16 terms the tensor core cuts its sum off, which loses up to 2^-23
+of it, always towards zero: 2^-27 of the value for each term that it sums alone, 8192 for an f16 result, 65536 for a
+bf16 one and 512 for an fp32 one or a segment of a longer sum.  Segments are added in fp32, each addition off by at
+most 2^-24 of the final sum.  The result is then rounded once, half a step."""
+import pytest
+import torch
+
+import fine_grained_moe_gemm_b200 as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, FH, FS = torch.bfloat16, torch.float16, torch.float32
+ALONE = {FH: 8192, BF: 65536, FS: 512}
+
+
+def _positive(gen, shape, dtype, scale=1.0, columns=True):
+    """Values in [scale / 2, 2 scale); with `columns` each column has a size of its own, so that the results lie
+    anywhere between two representable ones."""
+    t = torch.rand(shape, generator=gen, device=DEV).mul_(0.5).add_(0.5)
+    if columns:
+        t.mul_(torch.rand((1, shape[1]), generator=gen, device=DEV) + 1.0)
+    return t.mul_(scale).to(dtype)
+
+
+def _bound(terms, out):
+    """Relative: the cut-off sums, the segments' additions, the rounding."""
+    alone = ALONE[out]
+    loss = terms * 2.0 ** -27 if terms <= alone else 512 * 2.0 ** -27 + -(-terms // 512) * 2.0 ** -24
+    return (loss + 2.0 ** -24) * 1.01 + torch.finfo(out).eps / 2
+
+
+def _gradient(dy, x):
+    ref = torch.zeros((dy.shape[1], x.shape[1]), dtype=torch.float64, device=DEV)
+    for i in range(0, dy.shape[0], 1 << 18):
+        ref += dy[i:i + (1 << 18)].double().t() @ x[i:i + (1 << 18)].double()
+    return ref
+
+
+def _relative(got, ref, bound, what):
+    worst = float(((got.double() - ref) / ref).abs().max())
+    assert worst <= bound, f"{what}: {worst:.3g} of the value, {bound:.3g} allowed"
+
+
+def _offsets(sizes):
+    off = [0]
+    for m in sizes:
+        off.append(off[-1] + m)
+    return torch.tensor(off, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype,out,rows", [(FH, FH, 8192), (FH, FH, 8193), (FH, FH, 131077), (FH, FH, 1 << 20), (FH, FS, 131077),
+                                            (BF, BF, 65536), (BF, BF, 65537), (BF, BF, (1 << 20) + 3), (BF, BF, 1 << 22)])
+def test_long_gradients_of_one_sign(dtype, out, rows, accumulate):
+    """One long group among empty ones, so many that no tile's rows are shared out."""
+    gen = torch.Generator(device=DEV).manual_seed(rows)
+    groups, n, k = 300, 256, 128
+    sizes = [0] * groups
+    sizes[7] = rows
+    dy, x = _positive(gen, (rows, n), dtype, 4096.0 / rows), _positive(gen, (rows, k), dtype, columns=False)
+    dw = torch.full((groups, n, k), 2.0, dtype=out, device=DEV)
+    moe.moe_grouped_wgrad(dy, x, _offsets(sizes), dw, accumulate=accumulate)
+    assert moe.device_error() == 0
+    ref = _gradient(dy, x) + (2.0 if accumulate else 0.0)
+    _relative(dw[7], ref, _bound(rows, out), f"{rows} rows")
+    rest = torch.cat([dw[:7], dw[8:]])
+    assert bool((rest == (2.0 if accumulate else 0.0)).all())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,k", [(264, 328), (1032, 136), (8, 8), (256, 520)])
+def test_gradients_of_short_and_long_groups(n, k, accumulate):
+    """Groups on both sides of the length from which an f16 result takes segments, in one call."""
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    sizes = [20000, 100, 0, 8192, 30, 8200, 1] + [0] * 300 + [9000, 17]
+    rows = sum(sizes)
+    dy, x = _positive(gen, (rows, n), FH, 2.0 ** -4), _positive(gen, (rows, k), FH, columns=False)
+    dw = torch.full((len(sizes), n, k), 1.0, dtype=FH, device=DEV)
+    off = _offsets(sizes)
+    moe.moe_grouped_wgrad(dy, x, off, dw, accumulate=accumulate)
+    assert moe.device_error() == 0
+    start = off.tolist()
+    for g, m in enumerate(sizes):
+        if m == 0:
+            assert bool((dw[g] == (1.0 if accumulate else 0.0)).all())
+            continue
+        ref = _gradient(dy[start[g]:start[g + 1]], x[start[g]:start[g + 1]]) + (1.0 if accumulate else 0.0)
+        _relative(dw[g], ref, _bound(m, FH), f"group {g} of {m} rows")
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype,k", [(FH, 8192), (FH, 8200), (FH, 18432), (FH, 65536), (BF, 65536)])
+def test_long_products_of_one_sign(dtype, k, transpose, accumulate):
+    """Wide outputs, so that no tile's sum is shared out."""
+    gen = torch.Generator(device=DEV).manual_seed(k)
+    rows, n = 9480, 2056
+    x = _positive(gen, (rows, k), dtype, 4096.0 / k, columns=False)
+    w = (torch.rand((1, 1, n) if transpose else (1, n, 1), generator=gen, device=DEV) + 1.0)
+    w = (w * (torch.rand((1, k, n) if transpose else (1, n, k), generator=gen, device=DEV) * 0.5 + 0.5)).to(dtype)
+    y = torch.full((rows, n), 2.0, dtype=dtype, device=DEV)
+    moe.moe_grouped_mm(x, w, _offsets([rows]), y, transpose_w=transpose, accumulate=accumulate)
+    assert moe.device_error() == 0
+    at = torch.cat([torch.arange(0, 300), torch.arange(4096, 4400), torch.arange(rows - 100, rows)]).to(DEV)
+    w64 = w[0].double() if transpose else w[0].double().t()
+    ref = x[at].double() @ w64 + (2.0 if accumulate else 0.0)
+    _relative(y[at], ref, _bound(k, dtype), f"sums of {k}")
