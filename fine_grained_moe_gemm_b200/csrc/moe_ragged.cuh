@@ -525,6 +525,18 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
+// An integer sum times its two scales.  Their product alone can leave the normal numbers where the
+// result does not, so the sum meets the channel's scale first; z times it keeps its 24 bits (below
+// the normal numbers it is a multiple of their step, exact), and with |z| <= 2^30 it is finite below
+// RAG_SCALE_FIRST.  A larger scale comes last: if z times the row's overflows then, so does the result.
+// NaN and infinity come last too.  first * last is the scale, one of them 1.
+constexpr float RAG_SCALE_FIRST = 0x1p97f;
+__device__ __forceinline__ float rag_scale_first(float sw) { return fabsf(sw) < RAG_SCALE_FIRST ? sw : 1.0f; }
+__device__ __forceinline__ float rag_scale_last(float sw) { return fabsf(sw) < RAG_SCALE_FIRST ? 1.0f : sw; }
+__device__ __forceinline__ float rag_scaled(int z, float sx, float sw) {
+    return (float)z * rag_scale_first(sw) * sx * rag_scale_last(sw);
+}
+
 // Four values of a row, added to what is there with accumulate, rounded once.
 __device__ __forceinline__ void rag_store4(const RaggedArgs& P, size_t at, float4 s) {
     if (P.out == MOE_F32) {
@@ -599,8 +611,8 @@ __device__ __forceinline__ void rag_store_parts(const RaggedArgs& P, const uint8
                 if (I8) {
                     const float sx = __ldg(P.sx + row0 + r);
                     const float* sw = P.sw + (size_t)g * P.n + f0 + v * 4;
-                    s = make_float4((float)z.x * (sx * __ldg(sw)), (float)z.y * (sx * __ldg(sw + 1)),
-                                    (float)z.z * (sx * __ldg(sw + 2)), (float)z.w * (sx * __ldg(sw + 3)));
+                    s = make_float4(rag_scaled(z.x, sx, __ldg(sw)), rag_scaled(z.y, sx, __ldg(sw + 1)),
+                                    rag_scaled(z.z, sx, __ldg(sw + 2)), rag_scaled(z.w, sx, __ldg(sw + 3)));
                 }
                 rag_store4(P, (size_t)(row0 + r) * P.ldy + f0 + v * 4, s);
             }
@@ -634,6 +646,16 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
         "mov.b64 pa, {%0, %1};\n\t"
         "mov.b64 pb, {%2, %3};\n\t"
         "add.rn.f32x2 pa, pa, pb;\n\t"
+        "mov.b64 {%0, %1}, pa;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 pa, pb;\n\t"
+        "mov.b64 pa, {%0, %1};\n\t"
+        "mov.b64 pb, {%2, %3};\n\t"
+        "mul.rn.f32x2 pa, pa, pb;\n\t"
         "mov.b64 {%0, %1}, pa;\n\t}"
         : "+f"(a0), "+f"(a1)
         : "f"(b0), "f"(b1));
@@ -1049,7 +1071,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 }
                 continue;
             }
-            const float sw = sw_ahead;
+            const float first_scale = rag_scale_first(sw_ahead), last_scale = rag_scale_last(sw_ahead);
             if (AHEAD) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) scales[32 * c + lane] = sx_ahead[c];
@@ -1085,10 +1107,14 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
 #pragma unroll
                             for (int j = 0; j < 32; j += 4) {
                                 const float4 s4 = *reinterpret_cast<const float4*>(st + j);
-                                v[j] = (float)__float_as_int(v[j]) * (s4.x * sw);
-                                v[j + 1] = (float)__float_as_int(v[j + 1]) * (s4.y * sw);
-                                v[j + 2] = (float)__float_as_int(v[j + 2]) * (s4.z * sw);
-                                v[j + 3] = (float)__float_as_int(v[j + 3]) * (s4.w * sw);
+#pragma unroll
+                                for (int l = 0; l < 4; ++l) v[j + l] = (float)__float_as_int(v[j + l]);
+                                mul2(v[j], v[j + 1], first_scale, first_scale);
+                                mul2(v[j + 2], v[j + 3], first_scale, first_scale);
+                                mul2(v[j], v[j + 1], s4.x, s4.y);
+                                mul2(v[j + 2], v[j + 3], s4.z, s4.w);
+                                mul2(v[j], v[j + 1], last_scale, last_scale);
+                                mul2(v[j + 2], v[j + 3], last_scale, last_scale);
                             }
                         }
                         rag_store_rows(P, stage, it.row0 + c0, it.width - c0, f0, v);

@@ -404,7 +404,7 @@ MOE_API moe_status moe_quantize_int8(const void* x, moe_dtype dtype, int64_t ldx
                                      const int32_t* n_rows, int8_t* q, float* sx, moe_stream_t stream);
 
 /* y[r, j] (+)= sx[r] * sw[g, j] * sum_i q[r, i] w[g, j, i] for r in group g, the sum
- * exact.  q [rows, k] and w [groups, n, k] int8, sx [rows], sw [groups, n] fp32; y
+ * exact, the scales anywhere in fp32 (sx * sw may leave its range where y does not).  q [rows, k] and w [groups, n, k] int8, sx [rows], sw [groups, n] fp32; y
  * [rows, n] MOE_F32, MOE_BF16 or MOE_F16.  A dense layer is one group. */
 MOE_API moe_status moe_grouped_mm_int8(int groups, int rows, int n, int k, const int8_t* q, const float* sx,
                                        const int8_t* w, const float* sw, const int32_t* offsets, void* y, int64_t ldy,
