@@ -106,8 +106,12 @@ __device__ __forceinline__ int rag_items_of(const RaggedArgs& P, int rows) {
 }
 
 // Fills the table from the offsets (all THREADS threads of the CTA; the caller
-// synchronises).  A group whose offsets decrease or leave [0, rows] has no rows and sets
-// MOE_DEVERR_BAD_ROWS.
+// synchronises).  A group whose offsets decrease or leave [0, rows], or that starts before an
+// earlier group's end, has no rows and sets MOE_DEVERR_BAD_ROWS: groups never share rows, so no
+// two tiles store the same ones and the rows of all groups are at most `rows`, which bounds the
+// tiles that the host launches for.  Groups that share rows have a decrease between them, so
+// offsets without a bad group of their own need no more than the first look; else one thread
+// goes through them all.
 // `head` is what rag_first_offsets loaded: the caller does so before everything else, as the
 // loads' latency is most of what a CTA waits for before its first tile.
 __device__ __forceinline__ int2 rag_first_offsets(const RaggedArgs& P) {
@@ -122,6 +126,7 @@ __device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTa
     const int per = (P.groups + THREADS - 1) / THREADS;  // consecutive groups of a thread
     const int g0 = tid * per;
     int sum = 0;
+    bool bad = false;
     for (int g = g0; g < min(g0 + per, P.groups); ++g) {
         int a = head.x, b = head.y;  // per == 1: the thread's group
         if (per > 1) {
@@ -129,7 +134,7 @@ __device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTa
             b = __ldg(P.offsets + g + 1);
         }
         if (a < 0 || b < a || b > P.rows) {
-            if (blockIdx.x == 0) set_dev_error(MOE_DEVERR_BAD_ROWS);
+            bad = true;
             a = b = 0;
         }
         t.start[g] = a;
@@ -144,7 +149,22 @@ __device__ __forceinline__ void rag_build_table(const RaggedArgs& P, const RagTa
         if (lane >= o) incl += v;
     }
     if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
+    if (__syncthreads_or(bad)) {
+        if (tid != 0) return;
+        if (blockIdx.x == 0) set_dev_error(MOE_DEVERR_BAD_ROWS);
+        int end = 0, items = 0;
+        for (int g = 0; g < P.groups; ++g) {
+            int a = __ldg(P.offsets + g), b = __ldg(P.offsets + g + 1);
+            if (a < end || b < a || b > P.rows) a = b = 0;
+            else end = b;
+            t.start[g] = a;
+            t.count[g] = b - a;
+            t.first[g] = items;
+            items += items_of(b - a);
+        }
+        t.first[P.groups] = items;
+        return;
+    }
     int base = incl - sum;
     for (int w = 0; w < warp; ++w) base += warp_sums[w];
     for (int g = g0; g < min(g0 + per, P.groups); ++g) t.first[g] += base;

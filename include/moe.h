@@ -338,8 +338,9 @@ MOE_API moe_status moe_dense_ffn(int d, int hidden, moe_dtype act_dtype, moe_dty
  * buffer of `rows` rows.  offsets[0] may be above 0 and offsets[groups] below `rows`
  * (a block of experts, a buffer with room): rows outside are neither read into a
  * result nor written.  offsets = NULL with groups = 1: all rows.  Groups may be
- * empty.  A group whose offsets decrease or leave [0, rows] counts as empty and sets
- * MOE_DEVERR_BAD_ROWS.
+ * empty.  A group whose offsets decrease or leave [0, rows], or that starts before an
+ * earlier group's end, counts as empty and sets MOE_DEVERR_BAD_ROWS; the others are
+ * computed.  (With rows = 0 the offsets are not read.)
  *   - 1 <= groups <= 1024; rows <= 2^24; n, k multiples of 8 (8-bit operands: k of
  *     16), at most 65536.
  *   - ld*: elements from one row to the next, at least the row, a multiple of 16
