@@ -73,7 +73,7 @@ struct RagCfg {
     static constexpr int RING = STAGES * 2 * RAG_SLOT;
     static constexpr int TABLE = 3 * RAG_MAX_GROUPS * 4 + 16;  // first row, rows, first item of each group
     static constexpr int BARS = 2 * STAGES + (DIR == RAG_TN ? 2 * STAGES : 0) + 5;
-    static constexpr int MISC = (BARS * 8 + (2 + RAG_THREADS / 32) * 4 + 15) / 16 * 16;
+    static constexpr int MISC = (BARS * 8 + (3 + RAG_THREADS / 32) * 4 + 15) / 16 * 16;
     static constexpr int SMEM_BYTES = 1024 + RING + RAG_EPI_WARPS * (STAGING + SCALES) + TABLE + MISC;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 };
@@ -340,6 +340,29 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_
         if ((it & 63u) == 0) {
             if (*abort) return false;
             if (global_timer_ns() - t0 > limit_ns) {
+                set_dev_error(MOE_DEVERR_TIMEOUT);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// A wait that may begin many items before its own: the limit counts from the last change of
+// *progress (the item that the loads have come to), else as mbar_wait_bounded.
+__device__ __forceinline__ bool mbar_wait_following(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                    volatile int* progress, uint64_t limit_ns = 2000000000ull) {
+    int seen = *progress;
+    uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            const int now = *progress;
+            if (now != seen) {
+                seen = now;
+                t0 = global_timer_ns();
+            } else if (global_timer_ns() - t0 > limit_ns) {
                 set_dev_error(MOE_DEVERR_TIMEOUT);
                 *abort = 1;
                 return false;
@@ -743,7 +766,8 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     uint64_t* peer_done = landed + ST;     // TN, blocks with tail rows, leader: the peer's tail is zeroed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* warp_sums = reinterpret_cast<int*>(tmem_slot + 2);  // [RAG_THREADS / 32]
+    volatile int* progress = reinterpret_cast<volatile int*>(tmem_slot + 2);  // TN: the item being loaded
+    int* warp_sums = reinterpret_cast<int*>(tmem_slot + 3);  // [RAG_THREADS / 32]
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -760,6 +784,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
         fence_mbar_init();
     } else if (threadIdx.x == RAG_THREADS - 1) {
         *abort_flag = 0;
+        *progress = -1;
         tma_prefetch_desc(&P.a);
         tma_prefetch_desc(&P.b64);
         if (DIR != RAG_TN) {
@@ -802,6 +827,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                 RagWalk<DIR> walk(P, tab);
                 for (int i = first; i < total; i += n_clusters) {
                     const RagItem it = walk.at(i);
+                    if (DIR == RAG_TN && warp == 0) *progress = i;
                     const int blocks = rag_blocks<DIR, I8>(P, it);
                     const int f0 = it.m * 256 + (int)rank * 128;
                     const int nh = rag_mma_n<DIR>(it) / 2;  // this CTA's columns of the tile
@@ -925,8 +951,10 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
                     continue;
                 }
                 at.skip(mine - 1);
-                // every lane waits: each then sees the landed bytes before it overwrites some
-                const bool ok = mbar_wait_bounded(&landed[at.slot], (ph >> at.slot) & 1u, abort_flag);
+                // Items without tail rows are passed over at once, so this wait begins when the last
+                // tail was done and may span any number of them.
+                // Every lane waits: each then sees the landed bytes before it overwrites some.
+                const bool ok = mbar_wait_following(&landed[at.slot], (ph >> at.slot) & 1u, abort_flag, progress);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const int r0 = it.rows - (blocks - 1) * 64;  // rows of the group in this block
                 const int n = ((r0 + 15) & ~15) - r0;

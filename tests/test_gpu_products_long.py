@@ -107,3 +107,31 @@ def test_long_products_of_one_sign(dtype, k, transpose, accumulate):
     w64 = w[0].double() if transpose else w[0].double().t()
     ref = x[at].double() @ w64 + (2.0 if accumulate else 0.0)
     _relative(y[at], ref, _bound(k, dtype), f"sums of {k}")
+
+
+def test_tail_rows_after_seconds_of_work():
+    """Five rows behind a group of 425,984: two and a half seconds pass before the first block whose rows end inside
+    it, longer than any wait may stand still."""
+    torch.cuda.empty_cache()
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    width, period, times = 65536, 4096, 104
+    block = torch.randn((period, width), generator=gen, device=DEV, dtype=BF)
+    x = torch.empty((period * times + 5, width), dtype=BF, device=DEV)
+    x[:-5].view(times, period, width).copy_(block)
+    x[-5:].normal_(generator=gen)
+    dw = torch.empty((2, width, width), dtype=BF, device=DEV)
+    moe.moe_grouped_wgrad(x, x, _offsets([period * times, 5]), dw)
+    assert moe.device_error() == 0
+    half = torch.finfo(BF).eps / 2
+    for f0, c0 in ((0, 0), (width - 96, 1000), (30000, width - 200), (65280, 65280)):
+        f, c = slice(f0, f0 + 96), slice(c0, c0 + 200)
+        a, b = block[:, f].double(), block[:, c].double()
+        ref, mag = times * (a.t() @ b), times * (a.abs().t() @ b.abs())
+        terms = period * times
+        loss = (512 * 2.0 ** -27 + terms // 512 * 2.0 ** -24) * mag
+        assert bool(((dw[0, f, c].double() - ref).abs() <= loss * 1.01 + half * ref.abs()).all())
+        a, b = x[-5:, f].double(), x[-5:, c].double()
+        ref, mag = a.t() @ b, a.abs().t() @ b.abs()
+        assert bool(((dw[1, f, c].double() - ref).abs() <= 2.0 ** -23 * mag * 1.01 + half * ref.abs()).all())
+    del x, dw
+    torch.cuda.empty_cache()
