@@ -371,6 +371,15 @@ __device__ __forceinline__ bool mbar_wait_following(uint64_t* bar, uint32_t pari
     }
 }
 
+// Before a CTA that gave up a wait leaves: a role may have issued loads up to the moment when another
+// set the flag, and they must not land in the next CTA's memory.  A load lands within
+// microseconds, whatever its barrier is waiting for; a millisecond is the limit.
+__device__ __forceinline__ void settle_copies(volatile int* abort) {
+    if (!*abort) return;
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
 // fp32 -> 16-bit bits, one rounding to nearest even.
 template <bool BF16>
 __device__ __forceinline__ uint32_t rag_pack2(float a, float b) {
@@ -1195,6 +1204,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
 
     tc_fence_before();
     __syncthreads();
+    settle_copies(abort_flag);
     cluster_sync_all();  // no CTA leaves while its peer may still signal it or read its part
     if (warp == 4) {
         tc_fence_after();
