@@ -1380,6 +1380,13 @@ cudaError_t launch_ep_combine(const float* back, const int32_t* send_tok, int n_
     return cudaGetLastError();
 }
 
+// The status of a call that also leaves its error for the next cudaGetLastError, which would take
+// it for its own.
+static cudaError_t cleared(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 template <int DIR, bool I8, int MODE>
 static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_t s) {
     constexpr int smem = RagCfg<DIR>::SMEM_BYTES;
@@ -1391,13 +1398,13 @@ static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_
         if (MODE != RAG_PLAIN || I8) {  // the warps share out the registers of the launch: they must be there
             cudaFuncAttributes fa;
             cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
-            if (e != cudaSuccess) return e;
+            if (e != cudaSuccess) return cleared(e);
             if (fa.numRegs < RAG_REGS_LAUNCH) return cudaErrorInvalidConfiguration;
         }
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess && MODE == RAG_SPLIT)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) return cleared(e);
         if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchAttribute attr;
@@ -1412,7 +1419,7 @@ static cudaError_t launch_ragged_t(const RaggedArgs* args, int grid, cudaStream_
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     note_launch();
-    return cudaLaunchKernelEx(&cfg, kernel, *args);
+    return cleared(cudaLaunchKernelEx(&cfg, kernel, *args));
 }
 
 template <int DIR>
@@ -1448,7 +1455,7 @@ static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) return cleared(e);
         if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
     }
     args->stages = SPLIT_MAX_STAGES;
@@ -1465,7 +1472,7 @@ static cudaError_t launch_split_t(RaggedArgs* args, long long tiles, cudaStream_
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     note_launch();
-    return cudaLaunchKernelEx(&cfg, kernel, (const RaggedArgs)*args);
+    return cleared(cudaLaunchKernelEx(&cfg, kernel, (const RaggedArgs)*args));
 }
 
 const int* split_clusters() {

@@ -262,7 +262,9 @@ moe_status moe_grouped_wgrad(int groups, int rows, int n, int k, moe_dtype dtype
     if ((st = check_device(&di)) != MOE_OK) return st;
     if (rows == 0) {  // a sum of nothing
         if (accumulate) return MOE_OK;
-        return cuda_status(cudaMemsetAsync(dw, 0, dw_bytes, (cudaStream_t)stream));
+        const cudaError_t e = cudaMemsetAsync(dw, 0, dw_bytes, (cudaStream_t)stream);
+        if (e != cudaSuccess) cudaGetLastError();  // not left for the next call's check
+        return cuda_status(e);
     }
     RaggedArgs a;
     memset(&a, 0, sizeof(a));
