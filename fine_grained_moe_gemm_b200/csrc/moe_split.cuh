@@ -319,10 +319,10 @@ __global__ void __launch_bounds__(SPLIT_THREADS, 1) moe_split_kernel(const __gri
     if (P.split > 1) cluster_sync_all();  // no CTA leaves while another reads its part
     tc_fence_before();
     __syncthreads();
-    settle_copies(abort_flag);
     if (warp == 4) {
         tc_fence_after();
         tmem_dealloc<SPLIT_TMEM_COLS>(tmem_base);
+        settle_copies(abort_flag);
     }
 }
 
