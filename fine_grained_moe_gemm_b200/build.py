@@ -3,7 +3,7 @@
 checking build: table-dependent accesses are checked against their buffers
 and flagged with MOE_DEVERR_BOUNDS); and with g++ the Python module that
 marshals the short calls (``moe_binding.cpp``, host code against the installed
-torch, whose version its file name carries)."""
+torch and Python, whose versions its file name carries)."""
 from __future__ import annotations
 
 import os
@@ -30,9 +30,12 @@ BINDING_SOURCE = os.path.join(CSRC, "moe_binding.cpp")
 
 
 def binding_path() -> str:
+    """One file for each torch and each interpreter: the module is built against the headers of both."""
+    import sysconfig
+
     import torch
     version = "".join(c if c.isalnum() else "_" for c in torch.__version__)
-    return os.path.join(HERE, f"_binding_{version}.so")
+    return os.path.join(HERE, f"_binding_{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
