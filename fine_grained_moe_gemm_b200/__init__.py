@@ -661,7 +661,8 @@ _native = None
 
 def _binding():
     """The marshalling module, bound to the loaded library's entry points.  Like the library it is (re)built first
-    when it is missing or older than its sources; without it the call raises."""
+    when it is missing or older than its sources; where that fails the call raises: a module built against an older
+    include/moe.h would call the library with other arguments."""
     global _native
     if _native is None:
         import importlib.machinery
@@ -672,9 +673,8 @@ def _binding():
         try:
             path = _build.build_binding()
         except Exception as e:
-            path = _build.binding_path()
-            if not os.path.exists(path):
-                raise RuntimeError(f"{path} is missing and could not be built: {e}") from e
+            raise RuntimeError(f"{_build.binding_path()} is missing or older than its sources and could not be "
+                               f"built: {e}") from e
         loader = importlib.machinery.ExtensionFileLoader(__name__ + "._binding", path)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
         loader.exec_module(m)

@@ -38,6 +38,13 @@ def binding_path() -> str:
     return os.path.join(HERE, f"_binding_{version}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
+def binding_stale() -> bool:
+    """Whether the marshalling module is missing or older than its sources."""
+    path = binding_path()
+    deps = [BINDING_SOURCE, os.path.join(HERE, "..", "include", "moe.h")]
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps if os.path.exists(p))
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Builds the marshalling module when it is missing or older than its sources; returns its path."""
     import sysconfig
@@ -45,8 +52,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     import torch
 
     path = binding_path()
-    deps = [BINDING_SOURCE, os.path.join(HERE, "..", "include", "moe.h")]
-    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+    if not force and not binding_stale():
         return path
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
