@@ -172,10 +172,12 @@ _debug_lib = None
 
 
 def debug_lib():
-    """The checking build ``libmoe_b200_debug.so`` (the same entry points; kernels
-    check every table-dependent access against its buffer and flag
-    MOE_DEVERR_BOUNDS instead of touching memory outside it).  Built with the
-    regular library."""
+    """The checking build ``libmoe_b200_debug.so`` (the same entry points; the layer's
+    kernels check every access that depends on a device-built table against its
+    buffer and flag MOE_DEVERR_BOUNDS instead of touching memory outside it).  Built
+    with the regular library.  The products by group check their offsets in both
+    builds and their tables, which each CTA builds and reads itself, in neither; their
+    wrappers (``moe_grouped_mm`` and so on) call the regular library."""
     global _debug_lib
     lib()  # builds both libraries when they are stale
     with _lock:

@@ -53,10 +53,11 @@ constexpr int RAG_BAND = 8;               // chunks whose items run together (L2
 // loses up to 2^-23 of its value, always towards zero, so m terms of one sign come out small by up
 // to m * 2^-27 (measured: 6.4e-9 m, 6.7e-3 at 2^20 terms; terms of both signs about a sixth).
 // With PROMOTE the tensor core sums RAG_SEGMENT terms at a time and the epilogue adds the
-// segments in fp32 registers, rounding to nearest.  fp32 results take segments always, 16-bit
-// ones (RAG_LONG) in the groups where the loss could pass an eighth of their half step: segments
-// everywhere cost gradients of short groups their speed (32768 rows in 256 groups, 2048 x 7168 in
-// bf16: 2700 us, 2080 without).
+// segments in fp32 registers, rounding to nearest.  fp32 results take such segments always.  A 16-bit
+// one needs them only where the loss could pass an eighth of its half step, and then as long as that
+// (RAG_LONG: P.whole blocks).  With segments of 512 terms an f16 product of 4096 x 4096 x 18432 took
+// 479 us, with these or none 474; with segments for every 16-bit sum gradients of 32768 rows in 256
+// groups, 2048 x 7168 in bf16, took 2700 us in place of 2100.
 constexpr int RAG_SEGMENT = 512;
 // The segments' sums take 128 registers of an epilogue thread, so PROMOTE (and an int8
 // product, whose scales and next item go along: 2 % on short sums) moves
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(RAG_THREADS, 1) moe_ragged_kernel(const __grid
     const int total = tab.first[P.groups];
     const int first = SPLIT ? (int)cluster_id() : blockIdx.x >> 1;
     const int n_clusters = SPLIT ? 1 << 30 : gridDim.x >> 1;  // SPLIT: one item at most
-    constexpr int seg_blocks = I8 ? 1 << 30 : RAG_SEGMENT / 64;
+    const int seg_blocks = I8 ? 1 << 30 : MODE == RAG_LONG ? P.whole : RAG_SEGMENT / 64;
     // this pair's blocks of an item's
     auto begin = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part) : 0; };
     auto end = [&](int blocks) { return SPLIT ? rag_share(P, blocks, part + 1) : blocks; };

@@ -347,9 +347,12 @@ MOE_API moe_status moe_dense_ffn(int d, int hidden, moe_dtype act_dtype, moe_dty
  *     bytes; so halves of a wider buffer can be read and written in place.  Weights
  *     and their gradients are dense.
  *   - Outputs may not share bytes with inputs or with each other (MOE_ERR_INVALID_ARG;
- *     disjoint columns of one buffer are fine, a vector between the rows is not).  One launch, no workspace, results that do
- *     not depend on the run; sums in fp32 (8-bit operands: exact in 32 bits),
- *     rounded once.  accumulate = 1 adds to the output, before that rounding. */
+ *     disjoint columns of one buffer are fine, a vector between the rows is not).
+ *   - One launch, no workspace, results that do not depend on the run.
+ *   - Sums in fp32 (8-bit operands: exact in 32 bits), rounded once; accumulate = 1
+ *     adds to the output, before that rounding.  The tensor core cuts its sums off
+ *     towards zero: terms of one sign lose at most 4e-6 of an fp32 result and an
+ *     eighth of a half step of a 16-bit one, at any length. */
 
 /* y[r, :] (+)= x[r, :] . W_g^T for r in group g.  x [rows, k] and w of `dtype`
  * (MOE_BF16 or MOE_F16); y [rows, n] of the same type or MOE_F32.
@@ -586,7 +589,7 @@ MOE_API int moe_abi_version(void);
 
 /* ---- Checking build ------------------------------------------------------
  * The library also comes as libmoe_b200_debug.so, the same sources compiled
- * with MOE_DEBUG.  Its kernels check, before every access that depends on a
+ * with MOE_DEBUG.  The layer's kernels check, before every access that depends on a
  * device-built table, that the access stays inside its buffer: the permuted
  * row each token is copied to, the token of each row the combine adds into
  * y, the row count and the row range of every grouped-GEMM work item against

@@ -1,9 +1,9 @@
 """Long sums of the products by group, held to bounds that a lost block, a lost row or a bias would break.
 
 Tolerances of the sums of one sign.  After every 16 terms the tensor core cuts its sum off, which loses up to 2^-23
-of it, always towards zero: 2^-27 of the value for each term that it sums alone, 8192 for an f16 result, 65536 for a
-bf16 one and 512 for an fp32 one or a segment of a longer sum.  Segments are added in fp32, each addition off by at
-most 2^-24 of the final sum.  The result is then rounded once, half a step."""
+of it, always towards zero: 2^-27 of the value for each term that it sums alone, which are at most 8192 for an f16
+result, 65536 for a bf16 one and 512 for an fp32 one.  Longer sums take segments of that length, added in fp32, each
+addition off by at most 2^-24 of the final sum.  The result is then rounded once, half a step."""
 import pytest
 import torch
 
@@ -27,7 +27,7 @@ def _positive(gen, shape, dtype, scale=1.0, columns=True):
 def _bound(terms, out):
     """Relative: the cut-off sums, the segments' additions, the rounding."""
     alone = ALONE[out]
-    loss = terms * 2.0 ** -27 if terms <= alone else 512 * 2.0 ** -27 + -(-terms // 512) * 2.0 ** -24
+    loss = min(terms, alone) * 2.0 ** -27 + -(-terms // alone) * 2.0 ** -24
     return (loss + 2.0 ** -24) * 1.01 + torch.finfo(out).eps / 2
 
 
@@ -128,7 +128,7 @@ def test_tail_rows_after_seconds_of_work():
         a, b = block[:, f].double(), block[:, c].double()
         ref, mag = times * (a.t() @ b), times * (a.abs().t() @ b.abs())
         terms = period * times
-        loss = (512 * 2.0 ** -27 + terms // 512 * 2.0 ** -24) * mag
+        loss = (ALONE[BF] * 2.0 ** -27 + -(-terms // ALONE[BF]) * 2.0 ** -24) * mag
         assert bool(((dw[0, f, c].double() - ref).abs() <= loss * 1.01 + half * ref.abs()).all())
         a, b = x[-5:, f].double(), x[-5:, c].double()
         ref, mag = a.t() @ b, a.abs().t() @ b.abs()
